@@ -389,6 +389,179 @@ int mxgemm_validate_quantize(const void *X, int x_dtype, int64_t R, int64_t K, i
 int mxgemm_quantize(mxgemm_t h, const void *X, int x_dtype, int64_t R, int64_t K, int fmt,
                     uint8_t *codes, uint8_t *scales, hipStream_t stream);
 
+/* ---- products of codes with one fp32 scale per 128 K ---------------------
+ *
+ *   C[m,n] (+)= sum_b As[m,b] * Bs[n / b_rows, b] * sum_{k in b} dec(A[m,k]) * dec(B[n,k])
+ *
+ * over the blocks b = k / 128, for e4m3 / e5m2 codes: the form of checkpoints
+ * that carry one fp32 scale per 128 x 128 block of a weight (b_rows = 128)
+ * and per 128 consecutive elements of an activation's row.  b_rows = 1 gives
+ * B a scale per row and block as well: the weight gradient dW = dY^T X of a
+ * linear layer, both factors quantized along the tokens.
+ *   A        M x K codes, row-major; As  M x KB fp32, KB = ceil(K / 128);
+ *   B        N x K codes, K contiguous; Bs  ceil(N / b_rows) x KB fp32;
+ *   C        M x N fp32 or bf16, as for mxgemm_run.
+ * K is a multiple of 16 (the last block may be short), scales may be any
+ * fp32 numbers.
+ *
+ * Arithmetic, by the handle's variant (mxgemm_set_variant):
+ *   AUTO, LARGE, SKINNY   exact: the codes are widened to bf16 (exact), each
+ *       block is summed on the bf16 MFMA (exact products, one fp32 rounding
+ *       per 32 K) and joins the fp32 sum with its scales.  Error bound
+ *       (KB + 16) * 2^-24 * sum |a b|: 4 roundings in a block's sum, 3 of its
+ *       scales, one per block in the running sum, 8 where partial sums over
+ *       parts of K meet.
+ *   LARGE_NATIVE          the 256 x 256 kernel sums a block on the fp8 MFMA at
+ *       twice the rate; it drops what lies 13 bits below the largest of each
+ *       8 products (see the variants above), 2^-10 of a group's largest
+ *       product at most.  Shapes too small for that kernel run exact.
+ *   SKINNY_NATIVE         MXGEMM_ERR_VARIANT: small shapes are bound by
+ *       reading B and always run exact.
+ * LARGE and LARGE_NATIVE take the large tiles for M > 64 whatever the
+ * shape; SKINNY takes the small tiles whatever the shape.
+ * Needs no workspace and no operand buffer, keeps nothing between calls, and
+ * may be captured into a graph; calls on one handle may overlap.
+ *
+ * Checks (pure host): as for mxgemm_validate_args with K % 16 == 0, K >= 16,
+ * formats e4m3 / e5m2, b_rows 1 or 128 (MXGEMM_ERR_SHAPE), scales 4-byte
+ * aligned. */
+int mxgemm_validate_block128(const void *A, const float *A_scale, int fmtA,
+                             const void *B, const float *B_scale, int fmtB, int b_rows,
+                             const void *C, int64_t M, int64_t N, int64_t K,
+                             int use_acc, int out_dtype);
+int mxgemm_run_block128(mxgemm_t h, const void *A, const float *A_scale, int fmtA,
+                        const void *B, const float *B_scale, int fmtB, int b_rows,
+                        void *C, int64_t M, int64_t N, int64_t K,
+                        int use_acc, int out_dtype, hipStream_t stream);
+
+/* Quantization to such operands.  X is R x K, row-major, fp32 or bf16, K a
+ * multiple of 16.  Blocks are `rows` (1 or 128) rows by 128 columns; with
+ * a = max |x| of the block, at least 2^-100, the scale is a / MAX (448 for
+ * e4m3, 57344 for e5m2) and a code is x * (MAX / a) rounded to nearest even,
+ * each operation in fp32.
+ *   codes    R x K bytes, scales  ceil(R / rows) x ceil(K / 128) fp32;
+ *   codes_t  K x Rp bytes, Rp = R rounded up to 16: the transpose, whose
+ *            codes past R are zero, so that it is an operand with reduction
+ *            length Rp; scales_t  ceil(K / rows) x ceil(R / 128) fp32.
+ *            rows = 128: the same codes and scales, transposed (a weight for
+ *            the input gradient).  rows = 1: blocks of one column by 128 rows,
+ *            with scales of their own (an activation for the weight gradient).
+ * Either pair may be NULL (both pointers), not both pairs.  X is read once.
+ * A block holding a NaN or an infinity becomes NaN whole.
+ *
+ * Checks (pure host): rows, fmt, x_dtype, 1 <= R <= MXGEMM_MAX_M, 16 <= K <=
+ * MXGEMM_MAX_K, K % 16 == 0, R * K <= MXGEMM_MAX_QELEMS (with codes_t also
+ * R <= MXGEMM_MAX_K), X and codes 16-byte aligned, scales 4-byte aligned, all
+ * buffers disjoint. */
+int mxgemm_validate_quantize_block128(const void *X, int x_dtype, int64_t R, int64_t K, int rows,
+                                      int fmt, const uint8_t *codes, const float *scales,
+                                      const uint8_t *codes_t, const float *scales_t);
+int mxgemm_quantize_block128(mxgemm_t h, const void *X, int x_dtype, int64_t R, int64_t K, int rows,
+                             int fmt, uint8_t *codes, float *scales, uint8_t *codes_t,
+                             float *scales_t, hipStream_t stream);
+
+/* ---- key / value cache in 8 bits ------------------------------------------
+ *
+ * Keys and values of an attention layer as e4m3 codes in pages of page_size
+ * tokens, with one e8m0 scale byte per page and kv head (for keys and for
+ * values each).  Token t of a sequence is slot t % page_size of page
+ * page_table[s][t / page_size].
+ *   k_codes  pages x kv_heads x page_size x head_dim bytes
+ *   v_codes  pages x kv_heads x head_dim x page_size bytes: like the keys, the
+ *            products' second operand with its reduction (here the tokens)
+ *            contiguous
+ *   k_scales, v_scales  pages x kv_heads bytes
+ * Slots that hold no token may hold anything; a slot that holds one holds no
+ * NaN code (mxgemm_cache_append writes none).  head_dim is 64 or 128,
+ * page_size 16, 32, 64 or 128. */
+typedef struct mxgemm_cache {
+    uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+    int64_t pages;
+    int page_size, kv_heads, head_dim;
+} mxgemm_cache;
+
+/* A batch of sequences.  All arrays are device memory, read when the call
+ * runs, so that a captured call follows their values:
+ *   page_table  seqs x max_pages int32; an entry outside 0 .. pages - 1 hides
+ *               its tokens (not read, not written, seen by no query)
+ *   q_start     seqs + 1 int32, non-decreasing from 0 or more: the rows
+ *               q_start[s] .. q_start[s+1] - 1 of the call's token matrices
+ *               are sequence s's new tokens
+ *   ctx_len     seqs int32: the sequence's length with its new tokens, whose
+ *               positions are therefore ctx_len[s] - n .. ctx_len[s] - 1 for
+ *               n = q_start[s+1] - q_start[s].  Positions past the table's
+ *               reach (max_pages * page_size) hold nothing, positions below
+ *               zero see and write nothing.
+ * Host values: rows, the token matrices' row count (rows at or past it are
+ * never touched); max_q, a bound on n: new tokens past the first max_q of a
+ * sequence are ignored (their outputs left as they were); max_ctx, the longest
+ * ctx_len expected, which only shapes the launch. */
+typedef struct mxgemm_batch {
+    const int32_t *page_table, *q_start, *ctx_len;
+    int64_t seqs, max_pages, rows, max_q, max_ctx;
+} mxgemm_batch;
+
+/* Store the batch's new tokens.  K and V are rows x kv_heads x head_dim, fp32
+ * or bf16 (x_dtype), consecutive tokens kv_stride elements apart.  For each
+ * page that receives tokens, per head: b is the scale byte mxgemm_quantize
+ * gives the new values alone (MAX = 448); if the page held tokens of the
+ * sequence before them, the larger of b and the byte it had, and where that
+ * raises its byte the codes it held are rounded to the new scale (nearest,
+ * ties to even).  New codes are x * 2^(127 - byte) rounded likewise.  Other
+ * slots keep their codes.  New values holding a NaN or an infinity give the
+ * byte 255 (NaN): every query that sees a token of that page and head gets
+ * NaN there, until the page is started anew.
+ * A page that receives tokens must belong to one sequence of the batch.
+ *
+ * Checks (pure host): pointers, x_dtype, page_size, head_dim, 1 <= kv_heads
+ * <= 1024, 1 <= pages < 2^31, 1 <= seqs, rows, max_q, max_pages, max_ctx <
+ * 2^31, kv_stride >= kv_heads * head_dim and a multiple of 8, K, V and codes
+ * 16-byte aligned, int32 arrays 4-byte aligned; seqs * pages reached * kv_heads
+ * < 2^30.  No buffer that is written may overlap another. */
+int mxgemm_validate_cache_append(const mxgemm_cache *cache, const mxgemm_batch *batch,
+                                 const void *K, const void *V, int x_dtype, int64_t kv_stride);
+int mxgemm_cache_append(mxgemm_t h, const mxgemm_cache *cache, const mxgemm_batch *batch,
+                        const void *K, const void *V, int x_dtype, int64_t kv_stride,
+                        hipStream_t stream);
+
+/* Attention of the batch's new tokens (already appended) over the cache:
+ *
+ *   O[i, hq] = sum_j p_j v_j,  p = softmax_j (softmax_scale * q . k_j)
+ *
+ * over the keys j that the query at position p sees: j <= p, and, if window
+ * > 0, j > p - window or j < sinks.  Query head hq reads kv head
+ * hq / (q_heads / kv_heads).  A query that sees no key gets O = 0 and lse =
+ * -inf.  Q and O are rows x q_heads x head_dim bf16, tokens q_stride /
+ * o_stride elements apart; lse (optional) rows x q_heads fp32, the natural
+ * logarithm of the softmax's sum.  Rows outside every sequence are left as
+ * they were.
+ *
+ * Arithmetic: keys are widened exactly to bf16, scores, maximum, sum and
+ * output are fp32; the probabilities are rounded to bf16 (2^-9 relative) as
+ * the second product's operand, not in the sum.
+ *
+ * ws: mxgemm_cache_attention_workspace bytes, 256-byte aligned, lets few rows
+ * over long contexts be split over the GPU; NULL / 0 never splits.  Calls
+ * that share one must be ordered.  Its contents before a call do not matter.
+ * Keeps nothing between calls; captured calls follow the device arrays.
+ *
+ * Checks (pure host): those of the append where they apply; q_heads a
+ * multiple of kv_heads, at most 4096; q_stride, o_stride >= q_heads *
+ * head_dim, multiples of 8; Q, O 16-byte aligned; window, sinks >= 0, sinks
+ * only with a window; softmax_scale finite; ws aligned and large enough if given
+ * (MXGEMM_ERR_WORKSPACE). */
+int64_t mxgemm_cache_attention_workspace(const mxgemm_cache *cache, const mxgemm_batch *batch,
+                                         int q_heads, int64_t window);
+int mxgemm_validate_cache_attention(const mxgemm_cache *cache, const mxgemm_batch *batch,
+                                    const void *Q, int q_heads, int64_t q_stride,
+                                    float softmax_scale, int64_t window, int64_t sinks,
+                                    const void *O, int64_t o_stride, const float *lse,
+                                    const void *ws, size_t ws_bytes);
+int mxgemm_cache_attention(mxgemm_t h, const mxgemm_cache *cache, const mxgemm_batch *batch,
+                           const void *Q, int q_heads, int64_t q_stride, float softmax_scale,
+                           int64_t window, int64_t sinks, void *O, int64_t o_stride, float *lse,
+                           void *ws, size_t ws_bytes, hipStream_t stream);
+
 /* Streaming copy of `bytes` bytes from src to dst with raw buffer loads and
  * stores (the buffer_load / buffer_store example of the TLX global-memory
  * page), asynchronously on `stream`; both are device pointers on the

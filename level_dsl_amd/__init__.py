@@ -11,6 +11,7 @@ fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -68,12 +69,39 @@ SIGNATURES = {
                                   _i32, _i32, _vp]),
     "mxgemm_validate_quantize": (_i32, [_vp, _i32, _i64, _i64, _i32, _u8p, _u8p]),
     "mxgemm_quantize": (_i32, [_vp, _vp, _i32, _i64, _i64, _i32, _u8p, _u8p, _vp]),
+    "mxgemm_validate_block128": (_i32, [_vp, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _i64, _i64, _i64,
+                                        _i32, _i32]),
+    "mxgemm_run_block128": (_i32, [_vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _i64, _i64, _i64,
+                                   _i32, _i32, _vp]),
+    "mxgemm_validate_quantize_block128": (_i32, [_vp, _i32, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "mxgemm_quantize_block128": (_i32, [_vp, _vp, _i32, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),
+    "mxgemm_validate_cache_append": (_i32, [_vp, _vp, _vp, _vp, _i32, _i64]),
+    "mxgemm_cache_append": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _vp]),
+    "mxgemm_cache_attention_workspace": (_i64, [_vp, _vp, _i32, _i64]),
+    "mxgemm_validate_cache_attention": (_i32, [_vp, _vp, _vp, _i32, _i64, ctypes.c_float, _i64, _i64, _vp,
+                                               _i64, _vp, _vp, ctypes.c_size_t]),
+    "mxgemm_cache_attention": (_i32, [_vp, _vp, _vp, _vp, _i32, _i64, ctypes.c_float, _i64, _i64, _vp,
+                                      _i64, _vp, _vp, ctypes.c_size_t, _vp]),
     "mxgemm_validate_copy": (_i32, [_vp, _vp, ctypes.c_uint64]),
     "mxgemm_copy": (_i32, [_vp, _vp, _vp, ctypes.c_uint64, _vp]),
     "mxgemm_status_string": (ctypes.c_char_p, [_i32]),
 }
 
 _lib = None
+
+
+class CacheStruct(ctypes.Structure):
+    """mxgemm_cache."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+class BatchStruct(ctypes.Structure):
+    """mxgemm_batch."""
+    _fields_ = [("page_table", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
+                ("ctx_len", ctypes.c_void_p), ("seqs", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("max_q", ctypes.c_int64), ("max_ctx", ctypes.c_int64)]
 
 
 class MxgemmError(RuntimeError):
@@ -264,6 +292,83 @@ def mxgemm_quantize(h, X, x_dtype, R, K, fmt, codes, scales, stream=None) -> Non
         "mxgemm_quantize")
 
 
+def mxgemm_validate_block128(A, A_scale, fmtA, B, B_scale, fmtB, b_rows, C, M, N, K, use_acc,
+                             out_dtype) -> int:
+    """Returns the status code (0 = valid); pure host check."""
+    return load_library().mxgemm_validate_block128(
+        _ptr(A), _ptr(A_scale), int(fmtA), _ptr(B), _ptr(B_scale), int(fmtB), int(b_rows), _ptr(C),
+        int(M), int(N), int(K), int(use_acc), int(out_dtype))
+
+
+def mxgemm_run_block128(h, A, A_scale, fmtA, B, B_scale, fmtB, b_rows, C, M, N, K, use_acc, out_dtype,
+                        stream=None) -> None:
+    """C (+)= the product of codes with one fp32 scale per 128 K (B: per
+    b_rows x 128) on `stream` (default: torch's current stream)."""
+    _check(load_library().mxgemm_run_block128(
+        h, _ptr(A), _ptr(A_scale), int(fmtA), _ptr(B), _ptr(B_scale), int(fmtB), int(b_rows), _ptr(C),
+        int(M), int(N), int(K), int(use_acc), int(out_dtype), _stream(stream)), "mxgemm_run_block128")
+
+
+def mxgemm_validate_quantize_block128(X, x_dtype, R, K, rows, fmt, codes, scales, codes_t, scales_t) -> int:
+    """Returns the status code (0 = valid); pure host check."""
+    return load_library().mxgemm_validate_quantize_block128(
+        _ptr(X), int(x_dtype), int(R), int(K), int(rows), int(fmt), _ptr(codes), _ptr(scales),
+        _ptr(codes_t), _ptr(scales_t))
+
+
+def mxgemm_quantize_block128(h, X, x_dtype, R, K, rows, fmt, codes, scales, codes_t, scales_t,
+                             stream=None) -> None:
+    """Quantization of the R x K matrix X in blocks of `rows` x 128, and of
+    its transpose, on `stream` (default: torch's current stream); either
+    pair of outputs may be None."""
+    _check(load_library().mxgemm_quantize_block128(
+        h, _ptr(X), int(x_dtype), int(R), int(K), int(rows), int(fmt), _ptr(codes), _ptr(scales),
+        _ptr(codes_t), _ptr(scales_t), _stream(stream)), "mxgemm_quantize_block128")
+
+
+def _ref(x):
+    return None if x is None else ctypes.addressof(x)
+
+
+def mxgemm_validate_cache_append(cache, batch, K, V, x_dtype, kv_stride) -> int:
+    """Returns the status code (0 = valid); pure host check.  `cache` and
+    `batch` are a CacheStruct and a BatchStruct."""
+    return load_library().mxgemm_validate_cache_append(_ref(cache), _ref(batch), _ptr(K), _ptr(V),
+                                                       int(x_dtype), int(kv_stride))
+
+
+def mxgemm_cache_append(h, cache, batch, K, V, x_dtype, kv_stride, stream=None) -> None:
+    """Stores the batch's new tokens in the cache on `stream` (default:
+    torch's current stream)."""
+    _check(load_library().mxgemm_cache_append(h, _ref(cache), _ref(batch), _ptr(K), _ptr(V), int(x_dtype),
+                                              int(kv_stride), _stream(stream)), "mxgemm_cache_append")
+
+
+def mxgemm_cache_attention_workspace(cache, batch, q_heads, window=0) -> int:
+    """Bytes of the workspace that lets this call split its keys (0: it would
+    not split, -1: invalid arguments)."""
+    return int(load_library().mxgemm_cache_attention_workspace(_ref(cache), _ref(batch), int(q_heads),
+                                                               int(window)))
+
+
+def mxgemm_validate_cache_attention(cache, batch, Q, q_heads, q_stride, softmax_scale, window, sinks, O,
+                                    o_stride, lse, ws, ws_bytes) -> int:
+    """Returns the status code (0 = valid); pure host check."""
+    return load_library().mxgemm_validate_cache_attention(
+        _ref(cache), _ref(batch), _ptr(Q), int(q_heads), int(q_stride), float(softmax_scale), int(window),
+        int(sinks), _ptr(O), int(o_stride), _ptr(lse), _ptr(ws), int(ws_bytes))
+
+
+def mxgemm_cache_attention(h, cache, batch, Q, q_heads, q_stride, softmax_scale, window, sinks, O,
+                           o_stride, lse, ws, ws_bytes, stream=None) -> None:
+    """Attention of the batch's new tokens over the cache on `stream`
+    (default: torch's current stream)."""
+    _check(load_library().mxgemm_cache_attention(
+        h, _ref(cache), _ref(batch), _ptr(Q), int(q_heads), int(q_stride), float(softmax_scale),
+        int(window), int(sinks), _ptr(O), int(o_stride), _ptr(lse), _ptr(ws), int(ws_bytes),
+        _stream(stream)), "mxgemm_cache_attention")
+
+
 def mxgemm_validate_copy(dst, src, nbytes) -> int:
     """Returns the status code (0 = valid); pure host check."""
     return load_library().mxgemm_validate_copy(_ptr(dst), _ptr(src), int(nbytes))
@@ -398,3 +503,194 @@ class Gemm:
                              "scales (R, K/32) (preshuffled: rows padded to 32), uint8")
         mxgemm_quantize(self.h, X, xd, R, K, fmt, codes, scales, stream)
         return codes, scales
+
+    def block128(self, A, A_scale, fmtA, B, B_scale, fmtB, C, use_acc=False, stream=None):
+        """C (+)= (A * A_scale) @ (B * B_scale)^T for uint8 e4m3 / e5m2 codes A
+        (M, K) and B (N, K) with fp32 scales A_scale (M, ceil(K / 128)) and
+        B_scale (ceil(N / 128), ceil(K / 128)), or (N, ceil(K / 128)) for one
+        scale per row; C (M, N) float32 or bfloat16."""
+        if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
+            raise ValueError("A must be (M, K) and B (N, K)")
+        (M, K), N = A.shape, B.shape[0]
+        kb, nb = (K + 127) // 128, (N + 127) // 128
+        if A_scale.shape != (M, kb) or B_scale.shape not in ((nb, kb), (N, kb)):
+            raise ValueError("A_scale must be (M, ceil(K / 128)) and B_scale (ceil(N / 128), "
+                             "ceil(K / 128)) or (N, ceil(K / 128))")
+        if C.shape != (M, N) or C.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"C must be ({M}, {N}) float32 or bfloat16")
+        if A.dtype != torch.uint8 or B.dtype != torch.uint8 or A_scale.dtype != torch.float32 or \
+                B_scale.dtype != torch.float32:
+            raise ValueError("codes must be uint8 and scales float32")
+        _same_device(A, A_scale, B, B_scale, C)
+        for t in (A, A_scale, B, B_scale, C):
+            if not t.is_contiguous():
+                raise ValueError("all operands must be contiguous")
+        mxgemm_run_block128(self.h, A, A_scale, fmtA, B, B_scale, fmtB,
+                            128 if B_scale.shape[0] == nb else 1, C, M, N, K, int(bool(use_acc)),
+                            MXGEMM_OUT_F32 if C.dtype == torch.float32 else MXGEMM_OUT_BF16, stream)
+        return C
+
+    def quantize_block128(self, X, fmt, rows=1, normal=True, transposed=False, stream=None):
+        """Quantization of a contiguous (R, K) fp32 or bf16 device tensor in
+        blocks of `rows` (1 or 128) x 128: (codes (R, K), scales) if `normal`,
+        then (codes of the transpose (K, R rounded up to 16), their scales) if
+        `transposed`."""
+        if X.dim() != 2 or not X.is_contiguous() or X.device.type != "cuda":
+            raise ValueError("X must be a contiguous 2-D device tensor")
+        if X.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("X must be float32 or bfloat16")
+        if rows not in (1, 128):
+            raise ValueError("rows must be 1 or 128")
+        if not (normal or transposed):
+            raise ValueError("nothing to compute: normal and transposed are both off")
+        R, K = X.shape
+        kb, rb = (K + 127) // 128, (R + 127) // 128
+        out = []
+        with _on_stream(stream):
+            if normal:
+                out += [torch.empty((R, K), dtype=torch.uint8, device=X.device),
+                        torch.empty((R if rows == 1 else rb, kb), dtype=torch.float32, device=X.device)]
+            if transposed:
+                out += [torch.empty((K, (R + 15) // 16 * 16), dtype=torch.uint8, device=X.device),
+                        torch.empty((K if rows == 1 else kb, rb), dtype=torch.float32, device=X.device)]
+        c, s = out[:2] if normal else (None, None)
+        ct, st = out[-2:] if transposed else (None, None)
+        mxgemm_quantize_block128(self.h, X, MXGEMM_X_F32 if X.dtype == torch.float32 else MXGEMM_X_BF16,
+                                 R, K, rows, fmt, c, s, ct, st, stream)
+        return tuple(out)
+
+
+def _same_device(*tensors):
+    d = tensors[0].device
+    if d.type != "cuda" or any(t.device != d for t in tensors):
+        raise ValueError("all tensors must be on one GPU")
+
+
+def _on_stream(stream):
+    """The context in which a call on `stream` allocates, so that the memory
+    is not handed out again before that stream is done with it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    return torch.cuda.stream(stream)
+
+
+def _token_stride(t, heads: int, dim: int, what: str) -> int:
+    """Elements between the tokens of a (tokens, heads, dim) tensor whose
+    tokens are contiguous."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.stride(2) != 1 or \
+            (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{what} must be (tokens, {heads}, {dim}) with contiguous tokens")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+class Batch:
+    """The sequences of one step: page_table (S, max_pages), q_start (S + 1)
+    and ctx_len (S), int32 device tensors that the calls read when they run
+    (mxgemm_batch).  max_q bounds the new tokens of a sequence; max_ctx is
+    the longest context expected and only shapes the launch (default: the
+    page table's reach, given the cache)."""
+
+    def __init__(self, page_table, q_start, ctx_len, max_q: int, max_ctx: int = None):
+        if page_table.dim() != 2 or q_start.shape != (page_table.shape[0] + 1,) or \
+                ctx_len.shape != (page_table.shape[0],):
+            raise ValueError("page_table must be (S, max_pages), q_start (S + 1,), ctx_len (S,)")
+        _same_device(page_table, q_start, ctx_len)
+        for t in (page_table, q_start, ctx_len):
+            if t.dtype != torch.int32 or not t.is_contiguous():
+                raise ValueError("page_table, q_start and ctx_len must be contiguous int32")
+        self.tensors = (page_table, q_start, ctx_len)   # kept alive
+        self.max_q, self.max_ctx = int(max_q), max_ctx
+
+    def struct(self, cache, rows: int) -> BatchStruct:
+        t, q, c = self.tensors
+        if t.device != cache.device:
+            raise ValueError("the batch and the cache must be on one GPU")
+        reach = t.shape[1] * cache.page_size
+        return BatchStruct(t.data_ptr(), q.data_ptr(), c.data_ptr(), t.shape[0], t.shape[1], rows,
+                           self.max_q, reach if self.max_ctx is None else int(self.max_ctx))
+
+
+class KVCache:
+    """Keys and values of one attention layer as e4m3 codes in pages, one
+    e8m0 scale byte per page and kv head (mxgemm_cache).  The tensors are the
+    caller's: k_codes (pages, kv_heads, page_size, head_dim), v_codes (pages,
+    kv_heads, head_dim, page_size), k_scales and v_scales (pages, kv_heads),
+    all uint8."""
+
+    def __init__(self, gemm: Gemm, k_codes, k_scales, v_codes, v_scales):
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be (pages, kv_heads, page_size, head_dim)")
+        pages, heads, page, dim = k_codes.shape
+        if v_codes.shape != (pages, heads, dim, page) or k_scales.shape != (pages, heads) or \
+                v_scales.shape != (pages, heads):
+            raise ValueError("v_codes must be (pages, kv_heads, head_dim, page_size), the scales "
+                             "(pages, kv_heads)")
+        _same_device(k_codes, k_scales, v_codes, v_scales)
+        self.tensors = (k_codes, k_scales, v_codes, v_scales)
+        for t in self.tensors:
+            if t.dtype != torch.uint8 or not t.is_contiguous():
+                raise ValueError("codes and scales must be contiguous uint8")
+        self.gemm, self.device = gemm, k_codes.device
+        self.page_size, self.kv_heads, self.head_dim = page, heads, dim
+        self.struct = CacheStruct(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                                  v_scales.data_ptr(), pages, page, heads, dim)
+
+    @classmethod
+    def empty(cls, gemm: Gemm, pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda:0"):
+        """A cache of new tensors (zeros)."""
+        z = lambda *shape: torch.zeros(shape, dtype=torch.uint8, device=device)
+        return cls(gemm, z(pages, kv_heads, page_size, head_dim), z(pages, kv_heads),
+                   z(pages, kv_heads, head_dim, page_size), z(pages, kv_heads))
+
+    def append(self, batch: Batch, K, V, stream=None):
+        """Stores the batch's new tokens: K and V (tokens, kv_heads, head_dim),
+        float32 or bfloat16; tokens may lie further apart (views of a fused
+        projection)."""
+        stride = _token_stride(K, self.kv_heads, self.head_dim, "K")
+        if V.shape != K.shape or V.dtype != K.dtype or \
+                _token_stride(V, self.kv_heads, self.head_dim, "V") != stride:
+            raise ValueError("V must match K in shape, type and stride")
+        if K.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("K and V must be float32 or bfloat16")
+        if K.device != self.device or V.device != self.device:
+            raise ValueError("K, V and the cache must be on one GPU")
+        if K.shape[0] == 0:
+            return
+        mxgemm_cache_append(self.gemm.h, self.struct, batch.struct(self, K.shape[0]), K, V,
+                            MXGEMM_X_F32 if K.dtype == torch.float32 else MXGEMM_X_BF16, stride, stream)
+
+    def attend(self, batch: Batch, Q, scale: float = None, window: int = 0, sinks: int = 0, out=None,
+               lse=None, stream=None):
+        """Causal softmax attention of the batch's new tokens (appended
+        before) over the cache: Q (tokens, q_heads, head_dim) bfloat16 ->
+        (out like Q, lse (tokens, q_heads) float32).  scale defaults to
+        head_dim ** -0.5; window > 0 hides keys that far back or further,
+        except the first `sinks`.  Rows of out outside every sequence are not
+        written."""
+        if Q.dim() != 3 or Q.dtype != torch.bfloat16 or Q.device != self.device:
+            raise ValueError("Q must be a (tokens, q_heads, head_dim) bfloat16 tensor on the cache's GPU")
+        T, heads, dim = Q.shape
+        q_stride = _token_stride(Q, heads, self.head_dim, "Q")
+        with _on_stream(stream):
+            if out is None:
+                out = torch.empty((T, heads, dim), dtype=torch.bfloat16, device=Q.device)
+            if lse is None:
+                lse = torch.empty((T, heads), dtype=torch.float32, device=Q.device)
+            if out.shape != Q.shape or out.dtype != torch.bfloat16 or out.device != self.device or \
+                    lse.shape != (T, heads) or lse.dtype != torch.float32 or lse.device != self.device or \
+                    not lse.is_contiguous():
+                raise ValueError("out must be bfloat16 like Q, lse a contiguous (tokens, q_heads) float32")
+            o_stride = _token_stride(out, heads, dim, "out")
+            if T == 0:
+                return out, lse
+            b = batch.struct(self, T)
+            # a workspace of its own for each call: calls on several streams and
+            # captured graphs share none
+            n = mxgemm_cache_attention_workspace(self.struct, b, heads, window)
+            ws = torch.empty(n, dtype=torch.uint8, device=Q.device) if n > 0 else None
+            mxgemm_cache_attention(self.gemm.h, self.struct, b, Q, heads, q_stride,
+                                   self.head_dim ** -0.5 if scale is None else scale, window, sinks, out,
+                                   o_stride, lse, ws, max(n, 0), stream)
+        return out, lse

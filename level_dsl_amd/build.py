@@ -8,10 +8,12 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
-# the host side of the C ABI, then one translation unit per kernel family
+# the host sides of the C ABI (mx*.hip) and one translation unit per kernel family
 # (each holds that family's template instantiations), compiled in parallel
 SRCS = ["k_large_exact.hip", "k_large_exact_b.hip", "k_large_native.hip", "k_large_e2m1.hip",
-        "k_stream.hip", "k_skinny_fp8.hip", "k_skinny_e2m1.hip", "k_quant.hip", "mxgemm.hip"]
+        "k_stream.hip", "k_skinny_fp8.hip", "k_skinny_e2m1.hip", "k_quant.hip", "mxgemm.hip",
+        "k_block_small.hip", "k_block_quant.hip", "k_cache.hip", "k_attn_decode.hip",
+        "mxblock.hip", "mxcache.hip"]
 OUT = os.path.join(HERE, "libmxgemm.so")
 ARCH = "gfx950"
 

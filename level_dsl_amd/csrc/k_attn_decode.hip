@@ -1,0 +1,26 @@
+// k_attn_decode.hip -- attention over the 8-bit cache for few query rows.
+#include "mxattn_decode.h"
+
+namespace mxg {
+namespace {
+
+template <int D>
+hipError_t go(const cache::AttnArgs &a, hipStream_t s)
+{
+    static_assert(attn::ROWS == kDecodeRows, "host and kernel agree on a row tile");
+    const int64_t tiles = (int64_t)a.c.seqs * a.c.kv_heads * a.row_tiles;
+    hipLaunchKernelGGL((attn::decode_kernel<D>), dim3((unsigned)(tiles * a.splits)), dim3(attn::THREADS), 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1) return e;
+    hipLaunchKernelGGL((attn::join_kernel<D>), dim3((unsigned)tiles), dim3(attn::THREADS), 0, s, a);
+    return hipGetLastError();
+}
+
+} // namespace
+
+hipError_t launch_attn_decode(int head_dim, const cache::AttnArgs &a, hipStream_t s)
+{
+    return head_dim == 128 ? go<128>(a, s) : go<64>(a, s);
+}
+
+} // namespace mxg

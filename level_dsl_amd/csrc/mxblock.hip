@@ -1,0 +1,116 @@
+// mxblock.hip -- host side of the operators whose codes carry one fp32 scale
+// per 128 elements: argument checks, the choice of kernel and the launch.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "mxblock.h"
+#include "mxgemm.h"
+#include "mxgemm_ctx.h"
+
+using mxg::overlaps;
+
+extern "C" {
+
+int mxgemm_validate_block128(const void *A, const float *A_scale, int fmtA, const void *B,
+                             const float *B_scale, int fmtB, int b_rows, const void *C, int64_t M,
+                             int64_t N, int64_t K, int use_acc, int out_dtype)
+{
+    if (!A || !A_scale || !B || !B_scale || !C) return MXGEMM_ERR_NULL;
+    if ((fmtA != MXGEMM_FMT_E4M3 && fmtA != MXGEMM_FMT_E5M2) ||
+        (fmtB != MXGEMM_FMT_E4M3 && fmtB != MXGEMM_FMT_E5M2))
+        return MXGEMM_ERR_FMT;
+    if ((out_dtype != MXGEMM_OUT_F32 && out_dtype != MXGEMM_OUT_BF16) || (use_acc != 0 && use_acc != 1))
+        return MXGEMM_ERR_DTYPE;
+    if (b_rows != 1 && b_rows != 128) return MXGEMM_ERR_SHAPE;
+    if (M < 1 || N < 1 || K < 16 || M > MXGEMM_MAX_M || N > MXGEMM_MAX_N || K > MXGEMM_MAX_K ||
+        K % 16 != 0 || M * N > MXGEMM_MAX_MN)
+        return MXGEMM_ERR_SHAPE;
+    if (((uintptr_t)A | (uintptr_t)B | (uintptr_t)C) & 15u) return MXGEMM_ERR_ALIGN;
+    if (((uintptr_t)A_scale | (uintptr_t)B_scale) & 3u) return MXGEMM_ERR_ALIGN;
+    const uint64_t KB = (uint64_t)(K + 127) / 128, nb = (uint64_t)(N + b_rows - 1) / b_rows;
+    const uint64_t csize = (uint64_t)M * (uint64_t)N * (out_dtype == MXGEMM_OUT_F32 ? 4u : 2u);
+    if (overlaps(C, csize, A, (uint64_t)(M * K)) || overlaps(C, csize, B, (uint64_t)(N * K)) ||
+        overlaps(C, csize, A_scale, (uint64_t)M * KB * 4) || overlaps(C, csize, B_scale, nb * KB * 4))
+        return MXGEMM_ERR_ALIAS;
+    return MXGEMM_OK;
+}
+
+int mxgemm_run_block128(mxgemm_t h, const void *A, const float *A_scale, int fmtA, const void *B,
+                        const float *B_scale, int fmtB, int b_rows, void *C, int64_t M, int64_t N,
+                        int64_t K, int use_acc, int out_dtype, hipStream_t stream)
+{
+    if (!h || h->magic != mxg::kMagic) return MXGEMM_ERR_HANDLE;
+    int rc = mxgemm_validate_block128(A, A_scale, fmtA, B, B_scale, fmtB, b_rows, C, M, N, K, use_acc,
+                                      out_dtype);
+    if (rc != MXGEMM_OK) return rc;
+    if (h->variant == MXGEMM_VARIANT_SKINNY_NATIVE) return MXGEMM_ERR_VARIANT;
+    rc = mxg::check_device(h);
+    if (rc != MXGEMM_OK) return rc;
+
+    mxg::block::Args a;
+    a.A = (const uint8_t *)A;
+    a.As = A_scale;
+    a.B = (const uint8_t *)B;
+    a.Bs = B_scale;
+    a.C = C;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.KB = (int)((K + 127) / 128);
+    a.tiles_m = a.tiles_n = 0;
+    a.use_acc = use_acc;
+    a.out_bf16 = out_dtype == MXGEMM_OUT_BF16;
+    a.c_vec = N % 8 == 0 ? 2 : (N % 4 == 0 ? 1 : 0);
+    return mxg::launch_block_small(2 * fmtA + fmtB, b_rows, a, stream) == hipSuccess ? MXGEMM_OK
+                                                                                      : MXGEMM_ERR_HIP;
+}
+
+int mxgemm_validate_quantize_block128(const void *X, int x_dtype, int64_t R, int64_t K, int rows, int fmt,
+                                      const uint8_t *codes, const float *scales, const uint8_t *codes_t,
+                                      const float *scales_t)
+{
+    if (!X || (!codes != !scales) || (!codes_t != !scales_t) || (!codes && !codes_t)) return MXGEMM_ERR_NULL;
+    if (fmt != MXGEMM_FMT_E4M3 && fmt != MXGEMM_FMT_E5M2) return MXGEMM_ERR_FMT;
+    if (x_dtype != MXGEMM_X_F32 && x_dtype != MXGEMM_X_BF16) return MXGEMM_ERR_DTYPE;
+    if (rows != 1 && rows != 128) return MXGEMM_ERR_SHAPE;
+    if (R < 1 || K < 16 || R > MXGEMM_MAX_M || K > MXGEMM_MAX_K || K % 16 != 0 || R * K > MXGEMM_MAX_QELEMS ||
+        (codes_t && R > MXGEMM_MAX_K))
+        return MXGEMM_ERR_SHAPE;
+    if (((uintptr_t)X | (uintptr_t)codes | (uintptr_t)codes_t) & 15u) return MXGEMM_ERR_ALIGN;
+    if (((uintptr_t)scales | (uintptr_t)scales_t) & 3u) return MXGEMM_ERR_ALIGN;
+    const uint64_t kb = (uint64_t)(K + 127) / 128, rb = (uint64_t)(R + 127) / 128, r = (uint64_t)R, k = (uint64_t)K;
+    const void *ptr[5] = {X, codes, scales, codes_t, scales_t};
+    const uint64_t bytes[5] = {r * k * (x_dtype == MXGEMM_X_F32 ? 4u : 2u), r * k, (rows == 1 ? r : rb) * kb * 4,
+                               k * ((r + 15) / 16 * 16), (rows == 1 ? k : kb) * rb * 4};
+    for (int i = 0; i < 5; ++i)
+        for (int j = 0; j < i; ++j)
+            if (ptr[i] && ptr[j] && overlaps(ptr[i], bytes[i], ptr[j], bytes[j])) return MXGEMM_ERR_ALIAS;
+    return MXGEMM_OK;
+}
+
+int mxgemm_quantize_block128(mxgemm_t h, const void *X, int x_dtype, int64_t R, int64_t K, int rows, int fmt,
+                             uint8_t *codes, float *scales, uint8_t *codes_t, float *scales_t,
+                             hipStream_t stream)
+{
+    if (!h || h->magic != mxg::kMagic) return MXGEMM_ERR_HANDLE;
+    int rc = mxgemm_validate_quantize_block128(X, x_dtype, R, K, rows, fmt, codes, scales, codes_t, scales_t);
+    if (rc != MXGEMM_OK) return rc;
+    rc = mxg::check_device(h);
+    if (rc != MXGEMM_OK) return rc;
+    mxg::block::QuantArgs a;
+    a.X = (const uint8_t *)X;
+    a.codes = codes;
+    a.scales = scales;
+    a.codes_t = codes_t;
+    a.scales_t = scales_t;
+    a.R = R;
+    a.Rp = (R + 15) / 16 * 16;
+    a.K = (int)K;
+    a.KB = (int)((K + 127) / 128);
+    a.RB = (R + 127) / 128;
+    const int sel = 4 * fmt + (x_dtype == MXGEMM_X_BF16 ? 2 : 0) + (rows == 128 ? 1 : 0);
+    return mxg::launch_block_quant(sel, a, stream) == hipSuccess ? MXGEMM_OK : MXGEMM_ERR_HIP;
+}
+
+} // extern "C"

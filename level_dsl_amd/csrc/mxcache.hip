@@ -1,0 +1,241 @@
+// mxcache.hip -- host side of the 8-bit key / value cache: argument checks,
+// the choice of kernel and splits, and the launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "mxcache.h"
+#include "mxgemm.h"
+#include "mxgemm_ctx.h"
+
+using mxg::overlaps;
+
+namespace {
+
+constexpr int64_t kMaxInt = ((int64_t)1 << 31) - 1;
+constexpr int64_t kMaxGrid = (int64_t)1 << 30;
+
+int page_shift(int page_size)
+{
+    switch (page_size) {
+    case 16: return 4;
+    case 32: return 5;
+    case 64: return 6;
+    case 128: return 7;
+    default: return -1;
+    }
+}
+
+bool count_ok(int64_t x) { return x >= 1 && x <= kMaxInt; }
+
+uint64_t code_bytes(const mxgemm_cache *c)
+{
+    return (uint64_t)c->pages * c->kv_heads * c->page_size * c->head_dim;
+}
+
+// what both entry points ask of the cache and the batch
+int check_common(const mxgemm_cache *c, const mxgemm_batch *b)
+{
+    if (!c || !b || !c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales || !b->page_table || !b->q_start ||
+        !b->ctx_len)
+        return MXGEMM_ERR_NULL;
+    if (page_shift(c->page_size) < 0 || (c->head_dim != 64 && c->head_dim != 128) || c->kv_heads < 1 ||
+        c->kv_heads > 1024 || !count_ok(c->pages) || !count_ok(b->seqs) || !count_ok(b->max_pages) ||
+        !count_ok(b->rows) || !count_ok(b->max_q) || !count_ok(b->max_ctx))
+        return MXGEMM_ERR_SHAPE;
+    if (((uintptr_t)c->k_codes | (uintptr_t)c->v_codes) & 15u) return MXGEMM_ERR_ALIGN;
+    if (((uintptr_t)b->page_table | (uintptr_t)b->q_start | (uintptr_t)b->ctx_len) & 3u) return MXGEMM_ERR_ALIGN;
+    return MXGEMM_OK;
+}
+
+// whether [w, w + n) overlaps an array of the batch
+bool hits_batch(const void *w, uint64_t n, const mxgemm_batch *b)
+{
+    return overlaps(w, n, b->page_table, (uint64_t)b->seqs * b->max_pages * 4) ||
+           overlaps(w, n, b->q_start, ((uint64_t)b->seqs + 1) * 4) || overlaps(w, n, b->ctx_len, (uint64_t)b->seqs * 4);
+}
+
+mxg::cache::Pages pages_of(const mxgemm_cache *c, const mxgemm_batch *b)
+{
+    mxg::cache::Pages p;
+    p.k = c->k_codes;
+    p.ks = c->k_scales;
+    p.v = c->v_codes;
+    p.vs = c->v_scales;
+    p.table = b->page_table;
+    p.q_start = b->q_start;
+    p.ctx_len = b->ctx_len;
+    p.rows = b->rows;
+    p.pages = (int)c->pages;
+    p.max_pages = (int)b->max_pages;
+    p.seqs = (int)b->seqs;
+    p.max_q = (int)std::min(b->max_q, b->rows);
+    p.kv_heads = c->kv_heads;
+    p.shift = page_shift(c->page_size);
+    return p;
+}
+
+// pages that max_q new tokens of one sequence can reach
+int64_t append_steps(const mxgemm_cache *c, const mxgemm_batch *b)
+{
+    const int64_t q = std::min(b->max_q, b->rows);
+    return std::min((q + c->page_size - 2) / c->page_size + 1, b->max_pages);
+}
+
+int64_t row_tiles(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads)
+{
+    const int64_t rows = std::min(b->max_q, b->rows) * (q_heads / c->kv_heads);
+    return (rows + mxg::kDecodeRows - 1) / mxg::kDecodeRows;
+}
+
+// Splits of the visible keys: enough workgroups for two on each of the 256
+// CUs, but at least four 64-key blocks (one per wave) a split.
+int choose_splits(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads, int64_t window)
+{
+    const int64_t tiles = b->seqs * c->kv_heads * row_tiles(c, b, q_heads);
+    const int64_t reach = std::min(b->max_ctx, b->max_pages * c->page_size);
+    const int64_t keys = window ? std::min(reach, window + std::min(b->max_q, b->rows)) : reach;
+    const int64_t blocks = (keys + 63) / 64;
+    int64_t s = (512 + tiles - 1) / tiles;
+    s = std::min({s, blocks / 4, (int64_t)64});
+    return (int)std::max<int64_t>(s, 1);
+}
+
+int64_t workspace(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads, int splits)
+{
+    if (splits == 1) return 0;
+    return b->seqs * c->kv_heads * row_tiles(c, b, q_heads) * splits * mxg::kDecodeRows * (c->head_dim + 2) * 4;
+}
+
+bool heads_ok(const mxgemm_cache *c, int q_heads)
+{
+    return q_heads >= 1 && q_heads <= 4096 && q_heads % c->kv_heads == 0;
+}
+
+bool grid_ok(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads)
+{
+    // 2^31 tokens times 4096 heads fit 64 bits; the product of three counts may not
+    const int64_t t = row_tiles(c, b, q_heads);
+    return t <= kMaxGrid && b->seqs * c->kv_heads <= kMaxGrid / t;
+}
+
+} // namespace
+
+extern "C" {
+
+int mxgemm_validate_cache_append(const mxgemm_cache *cache, const mxgemm_batch *batch, const void *K,
+                                 const void *V, int x_dtype, int64_t kv_stride)
+{
+    if (!K || !V) return MXGEMM_ERR_NULL;
+    const int rc = check_common(cache, batch);
+    if (rc != MXGEMM_OK) return rc;
+    if (x_dtype != MXGEMM_X_F32 && x_dtype != MXGEMM_X_BF16) return MXGEMM_ERR_DTYPE;
+    const int64_t width = (int64_t)cache->kv_heads * cache->head_dim;
+    if (kv_stride < width || kv_stride > kMaxInt || kv_stride % 8 != 0) return MXGEMM_ERR_SHAPE;
+    if (batch->seqs > kMaxGrid / (append_steps(cache, batch) * cache->kv_heads)) return MXGEMM_ERR_SHAPE;
+    if (((uintptr_t)K | (uintptr_t)V) & 15u) return MXGEMM_ERR_ALIGN;
+    const uint64_t x = ((uint64_t)(batch->rows - 1) * kv_stride + width) * (x_dtype == MXGEMM_X_F32 ? 4u : 2u);
+    const uint64_t n = code_bytes(cache), ns = (uint64_t)cache->pages * cache->kv_heads;
+    const void *w[4] = {cache->k_codes, cache->v_codes, cache->k_scales, cache->v_scales};
+    const uint64_t wn[4] = {n, n, ns, ns};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (overlaps(w[i], wn[i], w[j], wn[j])) return MXGEMM_ERR_ALIAS;
+        if (overlaps(w[i], wn[i], K, x) || overlaps(w[i], wn[i], V, x) || hits_batch(w[i], wn[i], batch))
+            return MXGEMM_ERR_ALIAS;
+    }
+    return MXGEMM_OK;
+}
+
+int mxgemm_cache_append(mxgemm_t h, const mxgemm_cache *cache, const mxgemm_batch *batch, const void *K,
+                        const void *V, int x_dtype, int64_t kv_stride, hipStream_t stream)
+{
+    if (!h || h->magic != mxg::kMagic) return MXGEMM_ERR_HANDLE;
+    int rc = mxgemm_validate_cache_append(cache, batch, K, V, x_dtype, kv_stride);
+    if (rc != MXGEMM_OK) return rc;
+    rc = mxg::check_device(h);
+    if (rc != MXGEMM_OK) return rc;
+    mxg::cache::AppendArgs a;
+    a.c = pages_of(cache, batch);
+    a.K = (const uint8_t *)K;
+    a.V = (const uint8_t *)V;
+    a.stride = kv_stride;
+    a.steps = (int)append_steps(cache, batch);
+    return mxg::launch_cache_append(x_dtype == MXGEMM_X_BF16, cache->head_dim, a, stream) == hipSuccess
+               ? MXGEMM_OK
+               : MXGEMM_ERR_HIP;
+}
+
+int64_t mxgemm_cache_attention_workspace(const mxgemm_cache *cache, const mxgemm_batch *batch, int q_heads,
+                                         int64_t window)
+{
+    if (check_common(cache, batch) != MXGEMM_OK || !heads_ok(cache, q_heads) || !grid_ok(cache, batch, q_heads) ||
+        window < 0)
+        return -1;
+    return workspace(cache, batch, q_heads, choose_splits(cache, batch, q_heads, window));
+}
+
+int mxgemm_validate_cache_attention(const mxgemm_cache *cache, const mxgemm_batch *batch, const void *Q,
+                                    int q_heads, int64_t q_stride, float softmax_scale, int64_t window,
+                                    int64_t sinks, const void *O, int64_t o_stride, const float *lse,
+                                    const void *ws, size_t ws_bytes)
+{
+    if (!Q || !O) return MXGEMM_ERR_NULL;
+    const int rc = check_common(cache, batch);
+    if (rc != MXGEMM_OK) return rc;
+    if (!heads_ok(cache, q_heads) || !grid_ok(cache, batch, q_heads)) return MXGEMM_ERR_SHAPE;
+    const int64_t width = (int64_t)q_heads * cache->head_dim;
+    if (q_stride < width || o_stride < width || q_stride > kMaxInt || o_stride > kMaxInt || q_stride % 8 != 0 ||
+        o_stride % 8 != 0 || window < 0 || sinks < 0 || (sinks > 0 && window == 0) || !std::isfinite(softmax_scale))
+        return MXGEMM_ERR_SHAPE;
+    if (((uintptr_t)Q | (uintptr_t)O) & 15u || (uintptr_t)lse & 3u) return MXGEMM_ERR_ALIGN;
+    const int64_t need = ws ? workspace(cache, batch, q_heads, choose_splits(cache, batch, q_heads, window)) : 0;
+    if (ws && (((uintptr_t)ws & 255u) || (uint64_t)need > ws_bytes)) return MXGEMM_ERR_WORKSPACE;
+    const uint64_t n = code_bytes(cache), ns = (uint64_t)cache->pages * cache->kv_heads;
+    const uint64_t qn = ((uint64_t)(batch->rows - 1) * q_stride + width) * 2;
+    const void *w[3] = {O, lse, need ? ws : nullptr};
+    const uint64_t wn[3] = {((uint64_t)(batch->rows - 1) * o_stride + width) * 2, (uint64_t)batch->rows * q_heads * 4,
+                            (uint64_t)need};
+    for (int i = 0; i < 3; ++i) {
+        if (!w[i]) continue;
+        for (int j = 0; j < i; ++j)
+            if (w[j] && overlaps(w[i], wn[i], w[j], wn[j])) return MXGEMM_ERR_ALIAS;
+        if (overlaps(w[i], wn[i], Q, qn) || overlaps(w[i], wn[i], cache->k_codes, n) ||
+            overlaps(w[i], wn[i], cache->v_codes, n) || overlaps(w[i], wn[i], cache->k_scales, ns) ||
+            overlaps(w[i], wn[i], cache->v_scales, ns) || hits_batch(w[i], wn[i], batch))
+            return MXGEMM_ERR_ALIAS;
+    }
+    return MXGEMM_OK;
+}
+
+int mxgemm_cache_attention(mxgemm_t h, const mxgemm_cache *cache, const mxgemm_batch *batch, const void *Q,
+                           int q_heads, int64_t q_stride, float softmax_scale, int64_t window, int64_t sinks,
+                           void *O, int64_t o_stride, float *lse, void *ws, size_t ws_bytes, hipStream_t stream)
+{
+    if (!h || h->magic != mxg::kMagic) return MXGEMM_ERR_HANDLE;
+    int rc = mxgemm_validate_cache_attention(cache, batch, Q, q_heads, q_stride, softmax_scale, window, sinks, O,
+                                             o_stride, lse, ws, ws_bytes);
+    if (rc != MXGEMM_OK) return rc;
+    rc = mxg::check_device(h);
+    if (rc != MXGEMM_OK) return rc;
+    mxg::cache::AttnArgs a;
+    a.c = pages_of(cache, batch);
+    a.Q = (const uint16_t *)Q;
+    a.O = (uint16_t *)O;
+    a.lse = lse;
+    a.q_stride = q_stride;
+    a.o_stride = o_stride;
+    a.q_heads = q_heads;
+    a.group = q_heads / cache->kv_heads;
+    a.scale_log2 = softmax_scale * 1.4426950408889634f;
+    a.window = window;
+    a.sinks = sinks;
+    a.row_tiles = (int)row_tiles(cache, batch, q_heads);
+    a.splits = ws ? choose_splits(cache, batch, q_heads, window) : 1;
+    a.ws = (float *)ws;
+    return mxg::launch_attn_decode(cache->head_dim, a, stream) == hipSuccess ? MXGEMM_OK : MXGEMM_ERR_HIP;
+}
+
+} // extern "C"

@@ -14,6 +14,7 @@
 #include <new>
 
 #include "mxgemm.h"
+#include "mxgemm_ctx.h"
 #include "mxgemm_large.h"
 #include "mxgemm_launch.h"
 #include "mxgemm_skinny.h"
@@ -21,18 +22,6 @@
 
 static_assert(mxg::stream::BN == mxg::skinny::BN && mxg::stream::MAX_M == mxg::skinny::MAX_M,
               "both small-M kernels tile N and bound M alike");
-
-struct mxgemm_ctx {
-    uint32_t magic;
-    int device;
-    int variant;
-    int splits;      // 0 automatic, 1 never, S >= 2 forced
-    uint8_t *ws;     // caller's split-K workspace, or NULL
-    size_t ws_bytes;
-    int scale_layout;  // MXGEMM_SCALES_*
-    uint8_t *opbuf;    // caller's buffer for widened operands, or NULL
-    size_t opbuf_bytes;
-};
 
 // The split-K scratch of mxgemm_run_noalloc: 4 KiB of arrival counters, then
 // partial tiles, laid out like a caller's workspace of the same size.  Each
@@ -44,14 +33,9 @@ static __device__ __align__(256) uint8_t scratch[MXGEMM_NOALLOC_SCRATCH_BYTES];
 
 namespace {
 
-constexpr uint32_t kMagic = 0x4d584732u;  // "MXG2"
-constexpr uint32_t kDead = 0xdeadbeefu;
-
-bool overlaps(const void *a, uint64_t na, const void *b, uint64_t nb)
-{
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return x < y + nb && y < x + na;
-}
+using mxg::kDead;
+using mxg::kMagic;
+using mxg::overlaps;
 
 __global__ void zero_words(uint32_t *p, int n)
 {
