@@ -36,6 +36,8 @@ struct QuantArgs {
 
 // f = 2 fmtA + fmtB
 hipError_t launch_block_small(int f, int rows_b, const block::Args &a, hipStream_t s);  // k_block_small.hip
+hipError_t launch_block_native(int f, int rows_b, const block::Args &a, hipStream_t s); // k_block_native.hip
+hipError_t launch_block_exact(int f, int rows_b, const block::Args &a, hipStream_t s);  // k_block_exact.hip
 // sel = 4 fmt + 2 (bf16 input) + (rows == 128)
 hipError_t launch_block_quant(int sel, const block::QuantArgs &a, hipStream_t s);       // k_block_quant.hip
 

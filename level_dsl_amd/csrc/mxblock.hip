@@ -10,6 +10,19 @@
 
 using mxg::overlaps;
 
+namespace {
+
+// The large tiles, or the small ones: always the large for more than 64 rows
+// under the LARGE variants; under AUTO once their grid has enough workgroups.
+bool use_large(int variant, int64_t M, int64_t N)
+{
+    if (variant == MXGEMM_VARIANT_SKINNY || M <= 64) return false;
+    if (variant != MXGEMM_VARIANT_AUTO) return true;
+    return ((M + 255) / 256) * ((N + 127) / 128) >= 128;
+}
+
+} // namespace
+
 extern "C" {
 
 int mxgemm_validate_block128(const void *A, const float *A_scale, int fmtA, const void *B,
@@ -62,8 +75,14 @@ int mxgemm_run_block128(mxgemm_t h, const void *A, const float *A_scale, int fmt
     a.use_acc = use_acc;
     a.out_bf16 = out_dtype == MXGEMM_OUT_BF16;
     a.c_vec = N % 8 == 0 ? 2 : (N % 4 == 0 ? 1 : 0);
-    return mxg::launch_block_small(2 * fmtA + fmtB, b_rows, a, stream) == hipSuccess ? MXGEMM_OK
-                                                                                      : MXGEMM_ERR_HIP;
+    const int f = 2 * fmtA + fmtB;
+    const bool native = h->variant == MXGEMM_VARIANT_LARGE_NATIVE;
+    hipError_t e;
+    if (!use_large(h->variant, M, N))
+        e = mxg::launch_block_small(f, b_rows, a, stream);
+    else
+        e = native ? mxg::launch_block_native(f, b_rows, a, stream) : mxg::launch_block_exact(f, b_rows, a, stream);
+    return e == hipSuccess ? MXGEMM_OK : MXGEMM_ERR_HIP;
 }
 
 int mxgemm_validate_quantize_block128(const void *X, int x_dtype, int64_t R, int64_t K, int rows, int fmt,
