@@ -5,21 +5,21 @@
 namespace mxg {
 namespace {
 
-template <int FA, int FB, int ROWS_B, int MT, int CT>
+template <int FA, int FB, int ROWS_B, int MT, int CT, int W, int R>
 hipError_t go(block::Args a, hipStream_t s)
 {
     a.tiles_m = (a.M + 16 * MT - 1) / (16 * MT);
     a.tiles_n = (a.N + 16 * CT - 1) / (16 * CT);
-    hipLaunchKernelGGL((block_small::kernel<FA, FB, ROWS_B, MT, CT>),
-                       dim3((unsigned)((int64_t)a.tiles_m * a.tiles_n)), dim3(block_small::THREADS), 0, s, a);
+    hipLaunchKernelGGL((block_small::kernel<FA, FB, ROWS_B, MT, CT, W, R>),
+                       dim3((unsigned)((int64_t)a.tiles_m * a.tiles_n)), dim3(64 * W), 0, s, a);
     return hipGetLastError();
 }
 
 template <int FA, int FB>
 hipError_t pick(int rows_b, const block::Args &a, hipStream_t s)
 {
-    if (rows_b == 1) return a.M <= 16 ? go<FA, FB, 1, 1, 1>(a, s) : go<FA, FB, 1, 4, 2>(a, s);
-    return a.M <= 16 ? go<FA, FB, 128, 1, 1>(a, s) : go<FA, FB, 128, 4, 2>(a, s);
+    if (rows_b == 1) return a.M <= 16 ? go<FA, FB, 1, 1, 1, 8, 4>(a, s) : go<FA, FB, 1, 4, 2, 4, 3>(a, s);
+    return a.M <= 16 ? go<FA, FB, 128, 1, 1, 8, 4>(a, s) : go<FA, FB, 128, 4, 2, 4, 3>(a, s);
 }
 
 } // namespace

@@ -214,7 +214,7 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(block::Args p)
     wstore(0, win);
     auto sb_of = [&](int kt) MXG_INLINE -> float {
         if constexpr (ROWS_B == 1) return 0.0f;
-        return bs[min(kt, KB - 1)];
+        return scalar_load(bs + min(kt, KB - 1));
     };
     float sb = sb_of(0);
     wait_vmem();

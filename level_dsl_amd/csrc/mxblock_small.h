@@ -2,12 +2,15 @@
 // tiles: every shape, meant for those that leave the 256 x 256 tiles' grid
 // short (few rows, or few columns).
 //
-// One workgroup of 8 waves computes 16 MT rows by 16 CT columns of C.  The
-// waves split K: wave w takes blocks w, w + 8, ... of 128, so together they
-// read 1 KiB of a row at a time, each wave straight from global memory into
-// the MFMA operand registers (no operand byte is used by two waves, so LDS
-// would add a trip and nothing else).  Block sums meet in LDS at the end, in
-// wave order.
+// One workgroup of W waves computes 16 MT rows by 16 CT columns of C.  The
+// waves split K: wave w takes blocks w, w + W, ... of 128.  No operand byte is
+// used by two waves, so each runs on its own: a ring of R blocks in LDS,
+// filled by direct-to-LDS loads R - 1 blocks ahead, no barrier until the waves'
+// sums meet at the end, in wave order.  The loads go through LDS although
+// nothing is shared because of the address path: loading MFMA operands straight
+// into registers, neighbouring lanes read different rows, every 16 bytes a
+// cache-line lookup of its own (M = 64, N = 28672, K = 8192: 140 us); a
+// direct-to-LDS load reads whole 128-byte lines of 8 rows.
 //
 // One block b of 16 x 16 outputs: the codes are widened to bf16 (exact) and
 // summed by four 16x16x32 bf16 MFMAs into a fresh register tile, which joins
@@ -15,8 +18,9 @@
 // Roles as in the other kernels: B supplies the MFMA's rows and A its columns,
 // so a lane holds four consecutive columns of one row of C.
 // An MFMA sums over its K positions in any order, so lane group g = l / 16
-// takes bytes 16g .. +15 and 64 + 16g .. +15 of the block for both operands:
-// each load instruction reads 64 contiguous bytes per row.
+// takes chunks g and 4 + g (of 16 bytes) of a row for both operands.  Chunk c
+// of row r sits at position c ^ (r & 7) of its 128 bytes.  A's scales of a
+// block are one dword load (lane l: row l), handed out by lane exchanges.
 #pragma once
 
 #include "mxblock.h"
@@ -25,17 +29,33 @@
 namespace mxg {
 namespace block_small {
 
-constexpr int WAVES = 8, THREADS = 64 * WAVES;
+// Wait until every LDS read of this wave has returned.
+__device__ __forceinline__ void wait_lds()
+{
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
 
-template <int FA, int FB, int ROWS_B, int MT, int CT>
-__global__ __launch_bounds__(THREADS, 2) void kernel(block::Args p)
+template <int FA, int FB, int ROWS_B, int MT, int CT, int W, int R>
+__global__ __launch_bounds__(64 * W) void kernel(block::Args p)
 {
     static_assert(128 % (16 * CT) == 0, "a tile's columns share one 128-column block of scales");
+    static_assert(MT <= 4 && CT <= 4 && R >= 2 && R <= 4, "one lane per row of scales; four ring slots");
     constexpr int BM = 16 * MT, BN = 16 * CT;
-    __shared__ v4f red[WAVES][MT * CT][64];
+    constexpr int A_BYTES = BM * 128, STEP = (BM + BN) * 128;
+    constexpr int LOADS = 2 * (MT + CT) + (ROWS_B == 1 ? 2 : 1);  // vector-memory operations of one block
+    static_assert(MT * CT * 64 * 16 <= STEP, "the waves' sums fit one slot");
+    // one object per slot: a read of one then does not wait for loads into another
+    __shared__ __attribute__((aligned(1024))) uint8_t s0[W * STEP], s1[W * STEP], s2[R > 2 ? W * STEP : 16],
+        s3[R > 3 ? W * STEP : 16];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, g = lane >> 4;
+    auto slot = [&](auto S) MXG_INLINE -> uint8_t * {
+        constexpr int i = decltype(S)::value;
+        return (i == 0 ? s0 : i == 1 ? s1 : i == 2 ? s2 : s3) + wave * STEP;
+    };
     // rows fastest: the workgroups that share columns of B run together
     const int tm = blockIdx.x % p.tiles_m, tn = blockIdx.x / p.tiles_m;
     const int m0 = tm * BM, n0 = tn * BN;
@@ -47,36 +67,24 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(block::Args p)
     const float *const bs = p.Bs + (size_t)(ROWS_B == 1 ? n0 : n0 / 128) * KB;
     const rsrc_t rBs = make_rsrc(bs, ROWS_B == 1 ? (uint32_t)rows_b * KB * 4 : (uint32_t)KB * 4);
 
-    struct Raw {
-        v4i a[MT][2], b[CT][2];
-        float sa[MT];
-        float sb[ROWS_B == 1 ? CT : 1][ROWS_B == 1 ? 4 : 1];
+    struct Scales {
+        float a, b;  // lane l: row l's; b: column l's, or the tile's
     };
-    auto load = [&](int kb, Raw &r) MXG_INLINE {
-        // blocks past the end, and chunks past K in the last one, read as zero
+    const uint32_t chunk = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16, row8 = (uint32_t)(lane >> 3) * K;
+    // block kb into a slot; past the end of K everything reads as zero
+    auto load = [&](int kb, uint8_t *dst, Scales &sc) MXG_INLINE {
+        const uint32_t k = (uint32_t)kb * 128 + chunk;
+        const bool in = (int)k < K;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t k = (uint32_t)kb * 128 + 64 * h + 16 * g;
-            const bool in = (int)k < K;
+        for (int i = 0; i < 2 * MT; ++i) load16_lds(rA, dst + i * 1024, in ? row8 + (uint32_t)(8 * i) * K + k : kOob);
 #pragma unroll
-            for (int i = 0; i < MT; ++i) r.a[i][h] = load16(rA, in ? (uint32_t)(16 * i + r16) * K + k : kOob);
-#pragma unroll
-            for (int c = 0; c < CT; ++c) r.b[c][h] = load16(rB, in ? (uint32_t)(16 * c + r16) * K + k : kOob);
-        }
-        const bool in = kb < KB;
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-            r.sa[i] = __builtin_bit_cast(float, load4(rAs, in ? (uint32_t)((16 * i + r16) * KB + kb) * 4 : kOob));
-        if constexpr (ROWS_B == 1) {
-#pragma unroll
-            for (int c = 0; c < CT; ++c)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    r.sb[c][e] = __builtin_bit_cast(
-                        float, load4(rBs, in ? (uint32_t)((16 * c + 4 * g + e) * KB + kb) * 4 : kOob));
-        } else {
-            r.sb[0][0] = __builtin_bit_cast(float, load4(rBs, in ? (uint32_t)kb * 4 : kOob));
-        }
+        for (int i = 0; i < 2 * CT; ++i)
+            load16_lds(rB, dst + A_BYTES + i * 1024, in ? row8 + (uint32_t)(8 * i) * K + k : kOob);
+        sc.a = __builtin_bit_cast(float, load4(rAs, kb < KB && lane < BM ? (uint32_t)(lane * KB + kb) * 4 : kOob));
+        if constexpr (ROWS_B == 1)
+            sc.b = __builtin_bit_cast(float, load4(rBs, kb < KB && lane < BN ? (uint32_t)(lane * KB + kb) * 4 : kOob));
+        else
+            sc.b = scalar_load(bs + min(kb, KB - 1));
     };
 
     v4f acc[MT][CT];
@@ -85,49 +93,72 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(block::Args p)
 #pragma unroll
         for (int c = 0; c < CT; ++c) acc[i][c] = v4f{0.f, 0.f, 0.f, 0.f};
 
-    Raw cur, nxt;
-    load(wave, cur);
-    for (int kb = wave; kb < KB; kb += WAVES) {
-        load(kb + WAVES, nxt);
-        v8bf fa[MT][4];
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) decode16<FA>(cur.a[i][h], 1.0f, fa[i][2 * h], fa[i][2 * h + 1]);
+    const int sw = r16 & 7;
+    const uint32_t o0 = (uint32_t)(r16 * 128 + ((g ^ sw) << 4)), o1 = (uint32_t)(r16 * 128 + (((4 + g) ^ sw) << 4));
+    auto compute = [&](const uint8_t *src, const Scales &sc) MXG_INLINE {
+        v8bf fb[CT][4];
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
-            v8bf fb[4];
+            const uint8_t *q = src + A_BYTES + c * 16 * 128;
+            decode16<FB>(*reinterpret_cast<const v4i *>(q + o0), 1.0f, fb[c][0], fb[c][1]);
+            decode16<FB>(*reinterpret_cast<const v4i *>(q + o1), 1.0f, fb[c][2], fb[c][3]);
+        }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) decode16<FB>(cur.b[c][h], 1.0f, fb[2 * h], fb[2 * h + 1]);
+        for (int i = 0; i < MT; ++i) {
+            const uint8_t *q = src + i * 16 * 128;
+            v8bf fa[4];
+            decode16<FA>(*reinterpret_cast<const v4i *>(q + o0), 1.0f, fa[0], fa[1]);
+            decode16<FA>(*reinterpret_cast<const v4i *>(q + o1), 1.0f, fa[2], fa[3]);
+            float s = __shfl(sc.a, 16 * i + r16, 64);
+            if constexpr (ROWS_B != 1) s *= sc.b;
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
+            for (int c = 0; c < CT; ++c) {
                 v4f t = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int q = 0; q < 4; ++q) t = mfma_bf16_16(fb[q], fa[i][q], t);
-                if constexpr (ROWS_B == 1) {
+                for (int h = 0; h < 4; ++h) t = mfma_bf16_16(fb[c][h], fa[h], t);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[i][c][e] += t[e] * (cur.sa[i] * cur.sb[c][e]);
-                } else {
-                    const float s = cur.sa[i] * cur.sb[0][0];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[i][c][e] += t[e] * s;
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (ROWS_B == 1)
+                        acc[i][c][e] += t[e] * (s * __shfl(sc.b, 16 * c + 4 * g + e, 64));
+                    else
+                        acc[i][c][e] += t[e] * s;
                 }
             }
         }
-        cur = nxt;
+    };
+
+    Scales sc[R];
+    static_for<R - 1>([&](auto S) MXG_INLINE { load(wave + W * decltype(S)::value, slot(S), sc[decltype(S)::value]); });
+    // every wave runs the same number of rounds; blocks past K add zeros
+    const int steps = (KB + W - 1) / W;
+    for (int t0 = 0; t0 < steps; t0 += R) {
+        static_for<R>([&](auto S) MXG_INLINE {
+            constexpr int i = decltype(S)::value, n = (i + R - 1) % R;
+            const int t = t0 + i;
+            // block t - 1's slot is free: its reads have returned
+            wait_lds();
+            load(wave + W * (t + R - 1), slot(int_c<n>{}), sc[n]);
+            wait_vmcnt<(R - 1) * LOADS>();
+            __atomic_signal_fence(__ATOMIC_SEQ_CST);
+            compute(slot(S), sc[i]);
+        });
     }
 
+    wait_vmem();
+    wait_lds();
+    __syncthreads();
+    v4f *const red = reinterpret_cast<v4f *>(s0);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int c = 0; c < CT; ++c) red[wave][i * CT + c][lane] = acc[i][c];
+        for (int c = 0; c < CT; ++c) red[(wave * MT * CT + i * CT + c) * 64 + lane] = acc[i][c];
     __syncthreads();
     const int esz = p.out_bf16 ? 2 : 4;
     const rsrc_t rC = make_rsrc((uint8_t *)p.C + (size_t)m0 * p.N * esz, (uint32_t)rows_a * p.N * esz);
-    for (int t = wave; t < MT * CT; t += WAVES) {
-        v4f v = red[0][t][lane];
+    for (int t = wave; t < MT * CT; t += W) {
+        v4f v = red[t * 64 + lane];
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) v += red[w][t][lane];
+        for (int w = 1; w < W; ++w) v += red[(w * MT * CT + t) * 64 + lane];
         const int n = n0 + 16 * (t % CT) + 4 * g;
         store_c4(rC, (uint32_t)(16 * (t / CT) + r16) * p.N + n, n, p.N, v, p.out_bf16, p.use_acc, p.c_vec);
     }

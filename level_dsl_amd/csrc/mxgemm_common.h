@@ -120,6 +120,14 @@ __device__ __forceinline__ uint32_t opaque_s(uint32_t x)
     return x;
 }
 
+// *p through the scalar cache, for a wave-uniform address that nothing writes
+// while the kernel runs (the constant address space says so; a plain load
+// behind a direct-to-LDS load would be a vector load).
+__device__ __forceinline__ float scalar_load(const float *p)
+{
+    return *(const __attribute__((address_space(4))) float *)(uintptr_t)p;
+}
+
 // Wait until every vector-memory operation of this wave has completed,
 // including loads that write LDS directly, which the compiler does not
 // track (s_waitcnt vmcnt(0)).
