@@ -7,12 +7,16 @@ namespace {
 template <int D>
 hipError_t go(const cache::AttnArgs &a, hipStream_t s)
 {
-    static_assert(attn::ROWS == kDecodeRows, "host and kernel agree on a row tile");
+    static_assert(attn::ROWS == kDecodeRows && attn::MAX_SPLITS == kMaxSplits, "host and kernel agree");
     const int64_t tiles = (int64_t)a.c.seqs * a.c.kv_heads * a.row_tiles;
-    hipLaunchKernelGGL((attn::decode_kernel<D>), dim3((unsigned)(tiles * a.splits)), dim3(attn::THREADS), 0, s, a);
+    const dim3 grid((unsigned)(tiles * a.splits)), block(attn::THREADS);
+    if (a.c.shift < 6)
+        hipLaunchKernelGGL((attn::decode_kernel<D, true>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((attn::decode_kernel<D, false>), grid, block, 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
-    hipLaunchKernelGGL((attn::join_kernel<D>), dim3((unsigned)tiles), dim3(attn::THREADS), 0, s, a);
+    hipLaunchKernelGGL((attn::join_kernel<D>), dim3((unsigned)(tiles * attn::ROWS)), dim3(attn::JOIN_THREADS), 0, s, a);
     return hipGetLastError();
 }
 

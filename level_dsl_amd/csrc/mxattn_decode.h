@@ -1,8 +1,8 @@
 // mxattn_decode.h -- attention over the 8-bit cache for few query rows
-// (decode steps): the cache is streamed once, straight into MFMA operands.
+// (decode steps): the cache is streamed once, each block by one wave.
 //
 // A row is one (new token, query head of the group) pair of a sequence and kv
-// head, rows in token order; a workgroup of four waves takes 16 of them and a
+// head, rows in token order; a workgroup of two waves takes 16 of them and a
 // part of the visible keys (a split).  Keys come in blocks of 64, dealt to the
 // waves in turn.  Per block a wave computes
 //   S^T = K Q^T   16x16x32 bf16 MFMA, K's rows (tokens) by Q's columns (rows)
@@ -15,69 +15,49 @@
 // a lane's 4 tiles x 4 registers are then tokens 16 g .. 16 g + 15 (g = l /
 // 16) in order, which are also 16 contiguous bytes of each row of the
 // token-contiguous values.  Page sizes are multiples of 16, so such a chunk
-// has one page and one scale byte of keys and of values: the key's scale
-// multiplies the scores, the value's the probabilities, both in fp32.
+// has one page and one scale byte of keys and of values, which the widening
+// to bf16 applies: exact for bytes 10 .. 246.
+//
+// The waves share nothing until the end: each streams its blocks through LDS
+// buffers of its own (keys, values) by direct-to-LDS loads: whole lines, no
+// registers, no barrier.  A block's keys are loaded while the block before is
+// in its softmax and second product, its values behind that product; with two
+// waves per SIMD one computes while the other waits.  (Two buffers of both,
+// one wave per SIMD: 210 us where this takes 160 us, 64 sequences of 4097 to
+// 8192 tokens, 64 / 8 heads, dim 128: 5.1 TB/s.)  The running maximum lags: it moves, and
+// what was summed is scaled, only where a score passes it by more than 8
+// (log2), so that probabilities stay below 2^8; the result does not depend on
+// it.
 //
 // Masked scores are selected away after the product, and value codes no row of
 // the tile may see are zeroed before it, so what unwritten or foreign slots
-// hold never reaches a result.
+// hold never reaches a result.  Blocks that every row sees whole, with scale
+// bytes as above, skip both; the others apply the scales in fp32, to the
+// scores and the probabilities (byte 255 there makes NaN of what sees it).
 //
 // The waves' partial sums meet in LDS; with splits they go to the workspace
 // and a second kernel joins them (fixed order, so results repeat bit for
 // bit).  Bound by HBM: one read of every visible key and value.
 #pragma once
 
-#include "mxcache.h"
-#include "mxgemm_common.h"
+#include "mxattn.h"
+
+#include <type_traits>
 
 namespace mxg {
 namespace attn {
 
-using cache::AttnArgs;
-using cache::Pages;
-using cache::Seq;
+constexpr int WAVES = 4, THREADS = 64 * WAVES, ROWS = 16;
 
-constexpr int WAVES = 4, THREADS = 64 * WAVES, ROWS = 16, BLOCK = 64;
-constexpr float kNone = -__builtin_inff();
-
-// e8m0 byte -> 2^(s - 127) as used here: byte 255 is NaN
-__device__ __forceinline__ float scale_of(uint32_t s) { return e8m0_to_f32(s); }
-
-// 0xff in byte j of dword i where bit 4 i + j of m is set
-__device__ __forceinline__ uint32_t byte_mask(uint32_t m, int i)
-{
-    const uint32_t n = (m >> (4 * i)) & 15u;
-    return ((n & 1u) ? 0xffu : 0u) | ((n & 2u) ? 0xff00u : 0u) | ((n & 4u) ? 0xff0000u : 0u) |
-           ((n & 8u) ? 0xff000000u : 0u);
-}
-
-// The keys the rows with positions pmin .. pmax see together, as blocks: list
-// entry i is block i for i < sink_blocks, else first + (i - sink_blocks).
-struct Range {
-    int64_t lo, hi, sinks;       // visible: [lo, hi) and [0, sinks), sinks <= lo
-    int sink_blocks, first, count;
-    __device__ __forceinline__ int block(int i) const { return i < sink_blocks ? i : first + (i - sink_blocks); }
-};
-template <int BLK>
-__device__ __forceinline__ Range range_of(const AttnArgs &p, int ctx, int64_t pmin, int64_t pmax)
-{
-    Range r;
-    r.hi = max((int64_t)0, min((int64_t)ctx, pmax + 1));
-    r.lo = p.window ? max((int64_t)0, pmin - p.window + 1) : 0;
-    r.lo = min(r.lo, r.hi);
-    r.sinks = min(p.sinks, r.lo);
-    r.first = (int)(r.lo / BLK);
-    const int end = (int)((r.hi + BLK - 1) / BLK);
-    r.sink_blocks = min((int)((r.sinks + BLK - 1) / BLK), r.first);
-    r.count = r.hi > 0 ? r.sink_blocks + (end - r.first) : 0;
-    return r;
-}
-
-template <int D>
+template <int D, bool SMALL>
 __global__ __launch_bounds__(THREADS, 2) void decode_kernel(AttnArgs p)
 {
     constexpr int CH = D / 64;      // 16-byte key chunks per lane and token
     constexpr int DT = D / 16;      // 16-row tiles of O^T
+    using T = Tile<D>;
+    constexpr int HALF = T::HALF + 1;  // vector-memory operations of a block's keys, or values: loads, a scale byte
+    // separate objects: a read of one then does not wait for loads into the other
+    __shared__ __attribute__((aligned(1024))) uint8_t keys[WAVES * T::K_BYTES], values[WAVES * T::K_BYTES];
     const Pages &c = p.c;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, g = lane >> 4;
@@ -93,111 +73,197 @@ __global__ __launch_bounds__(THREADS, 2) void decode_kernel(AttnArgs p)
     const int64_t rows = (int64_t)q.n * G;
     const int64_t row0 = (int64_t)rt * ROWS;
     if (row0 >= rows) return;
-    const int64_t row_end = min(row0 + ROWS, rows);
-    const Range rg = range_of<BLOCK>(p, q.ctx, q.first + row0 / G, q.first + (row_end - 1) / G);
+    const int pmin = position(q, row0 / G), pmax = position(q, (min(row0 + ROWS, rows) - 1) / G);
+    const Range rg = range_of(p, q.ctx, pmin, pmax);
 
-    // this lane's column: a row of the tile
+    const int per = (rg.count + p.splits - 1) / p.splits;
+    const int b0 = sp * per + wave, b1 = min(rg.count, sp * per + per);
+
+    const uint32_t page1 = (uint32_t)D << c.shift, head_at = head * page1, page = page1 * c.kv_heads;
+    const int32_t *const table = c.table + (int64_t)s * c.max_pages;
+    uint8_t *const my_keys = keys + wave * T::K_BYTES, *const my_values = values + wave * T::K_BYTES;
+    uint32_t kb = 0, vb = 0;        // scale bytes: keys of chunk r16 / 4, values of chunk g
+    auto fetch_keys = [&](const Ids<SMALL> &ids, int t0) MXG_INLINE {
+        T::template load_keys<1>(c, ids, head_at, page, t0, 0, my_keys);
+        kb = c.ks[(size_t)max(ids.of(r16 >> 2), 0) * c.kv_heads + head];
+    };
+    auto fetch_values = [&](const Ids<SMALL> &ids, int t0) MXG_INLINE {
+        T::template load_values<1>(c, ids, head_at, page, t0, 0, my_values);
+        vb = c.vs[(size_t)max(ids.of(g), 0) * c.kv_heads + head];
+    };
+    Ids<SMALL> here = {}, next = {};
+    if (b0 < b1) {
+        here = ids_of<SMALL>(c, table, rg.start(b0), rg.hi);
+        fetch_keys(here, rg.start(b0));
+        fetch_values(here, rg.start(b0));
+        if (b0 + WAVES < b1) next = ids_of<SMALL>(c, table, rg.start(b0 + WAVES), rg.hi);
+    }
+
+    // this lane's column: a row of the tile.  A negative softmax scale goes
+    // into the sign of Q, so that the largest product is the largest score.
     const int64_t row = row0 + r16;
     const bool live = row < rows;
     const int qi = (int)((live ? row : row0) / G), qh = (int)((live ? row : row0) % G);
-    const int64_t pos = (int64_t)q.first + qi;
-    const int64_t wlo = p.window ? pos - p.window : -1;   // key > wlo is inside the window
+    const int pos = position(q, qi);
+    const int wlo = p.window ? pos - p.window : -0x7fffffff - 1;   // key > wlo is inside the window
+    const float scale = fabsf(p.scale_log2);
     v8bf qf[2 * CH];
     {
         const uint16_t *src = p.Q + (q.q0 + qi) * p.q_stride + (int64_t)(head * G + qh) * D;
+        const int flip = p.scale_log2 < 0.0f ? (int)0x80008000u : 0;
 #pragma unroll
         for (int h = 0; h < CH; ++h)
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-                qf[2 * h + u] = *reinterpret_cast<const v8bf *>(src + 64 * h + 16 * g + 8 * u);
+            for (int u = 0; u < 2; ++u) {
+                v4i x = *reinterpret_cast<const v4i *>(src + 64 * h + 16 * g + 8 * u);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] ^= flip;
+                qf[2 * h + u] = __builtin_bit_cast(v8bf, x);
+            }
     }
-
-    const int per = (rg.count + p.splits - 1) / p.splits;
-    const int b0 = sp * per, b1 = min(rg.count, b0 + per);
 
     v4f o[DT];
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = v4f{0.f, 0.f, 0.f, 0.f};
     float m = kNone, l = 0.0f;
 
-    const size_t page_bytes = (size_t)D << c.shift;
-    const int pmask = (1 << c.shift) - 1;
-    for (int i = b0 + wave; i < b1; i += WAVES) {
-        const int64_t t0 = (int64_t)rg.block(i) * BLOCK;
-        // chunk of this lane's key rows (r16 / 4) and of its values and scores (g)
-        const int64_t tk = t0 + 16 * (r16 >> 2), tv = t0 + 16 * g;
-        const int pk = tk < rg.hi ? cache::page_of(c, s, (int)(tk >> c.shift)) : -1;
-        const int pv = tv < rg.hi ? cache::page_of(c, s, (int)(tv >> c.shift)) : -1;
-        const size_t ak = (size_t)max(pk, 0) * c.kv_heads + head, av = (size_t)max(pv, 0) * c.kv_heads + head;
-        const float ks = scale_of(c.ks[av]) * p.scale_log2, vs = scale_of(c.vs[av]);
-
-        v4f st[4];
+    // scores of the block in my_keys, each key scaled by ks (chunk r16 / 4)
+    auto scores = [&](v4f (&st)[4], float ks) MXG_INLINE {
+        v8bf kf[4][2 * CH];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const uint8_t *src = c.k + ak * page_bytes + (size_t)(((int)tk & pmask) + 4 * t + (r16 & 3)) * D + 16 * g;
+            const int token = 16 * (r16 >> 2) + 4 * t + (r16 & 3);
+#pragma unroll
+            for (int h = 0; h < CH; ++h)
+                decode16<0>(*reinterpret_cast<const v4i *>(my_keys + T::key(token, 4 * h + g)), ks, kf[t][2 * h],
+                            kf[t][2 * h + 1]);
             st[t] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int h = 0; h < CH; ++h) {
-                v8bf lo, hi;
-                decode16<0>(*reinterpret_cast<const v4i *>(src + 64 * h), 1.0f, lo, hi);
-                st[t] = mfma_bf16_16(lo, qf[2 * h], st[t]);
-                st[t] = mfma_bf16_16(hi, qf[2 * h + 1], st[t]);
-            }
         }
-        float mx = kNone;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int h = 0; h < 2 * CH; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int64_t key = tv + 4 * t + e;
-                const bool see = pv >= 0 && key <= pos && key < rg.hi && (key > wlo || key < p.sinks);
-                st[t][e] = see ? st[t][e] * ks : kNone;
-                mx = fmaxf(mx, st[t][e]);   // a NaN score passes by: it makes the row's sum NaN
-            }
-        mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-        mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-        const float mn = fmaxf(m, mx);
-        const float mu = mn == kNone ? 0.0f : mn;
-        const float alpha = __builtin_amdgcn_exp2f(m - mu);
-        m = mn;
-        v8bf pf[2];
-        float sum = 0.0f;
+            for (int t = 0; t < 4; ++t) st[t] = mfma_bf16_16(kf[t][h], qf[h], st[t]);
+    };
+    // the running maximum follows a block's largest score
+    auto follow = [&](float mx) MXG_INLINE {
+        mx = max_groups(mx);
+        if (__builtin_amdgcn_ballot_w64(mx > m + 8.0f)) {
+            const float mn = fmaxf(m, mx), alpha = mn == kNone ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+            m = mn;
+            l *= alpha;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float x = __builtin_amdgcn_exp2f(st[t][e] - mu);
-                sum += x;
-                pf[t >> 1][4 * (t & 1) + e] = (__bf16)(st[t][e] == kNone ? 0.0f : x * vs);
-            }
-        l = l * alpha + sum;
-
-        // which of this lane's 16 value tokens some row of the tile sees
-        uint32_t keep = 0;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const int64_t key = tv + e;
-            keep |= (pv >= 0 && key < rg.hi && (key >= rg.lo || key < rg.sinks) ? 1u : 0u) << e;
+            for (int d = 0; d < DT; ++d) o[d] *= alpha;
         }
+        return m == kNone ? 0.0f : m;
+    };
+    // O^T += V^T P^T from my_values; keep: which of the lane's chunk counts
+    auto add = [&](auto EDGE, const v8bf (&pf)[2], float vs, uint32_t keep) MXG_INLINE {
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-            v4i x = *reinterpret_cast<const v4i *>(c.v + av * page_bytes +
-                                                   ((size_t)(16 * d + r16) << c.shift) + ((int)tv & pmask));
-#pragma unroll
-            for (int w = 0; w < 4; ++w) x[w] &= (int)byte_mask(keep, w);
+            v4i x = *reinterpret_cast<const v4i *>(my_values + T::value(16 * d + r16, g));
+            if constexpr (decltype(EDGE)::value) x = keep16(x, keep);
             v8bf lo, hi;
-            decode16<0>(x, 1.0f, lo, hi);
-            o[d] *= alpha;
+            decode16<0>(x, vs, lo, hi);
             o[d] = mfma_bf16_16(lo, pf[0], o[d]);
             o[d] = mfma_bf16_16(hi, pf[1], o[d]);
+        }
+    };
+
+    for (int i = b0; i < b1; i += WAVES) {
+        const int t0 = rg.start(i);
+        const bool more = i + WAVES < b1;
+        wait_vmcnt<HALF>();   // the keys; the values were loaded behind them
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        const uint32_t kb_now = kb;
+        auto next_keys = [&]() MXG_INLINE {   // the keys' reads have returned
+            wait_lds();
+            if (more) fetch_keys(next, rg.start(i + WAVES));
+        };
+        auto wait_values = [&]() MXG_INLINE {
+            if (more) wait_vmcnt<HALF>();
+            else wait_vmem();
+            __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        };
+        v4f st[4];
+        v8bf pf[2];
+        // the values' byte came behind the keys: it is waited for with the values
+        const bool whole = here.all() && t0 + BLOCK <= rg.hi && t0 + BLOCK - 1 <= pmin &&
+                           (!p.window || t0 > pmax - p.window) &&
+                           __builtin_amdgcn_ballot_w64(!plain_scale(kb_now)) == 0;
+        if (whole) {
+            scores(st, e8m0_to_f32(kb_now));
+            next_keys();
+            float mx = kNone;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx = fmaxf(mx, st[t][e]);   // a NaN score passes by: it makes the sum NaN
+            const float mu = follow(mx * scale);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    st[t][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(st[t][e], scale, -mu));
+                    l += st[t][e];
+                }
+        } else {
+            scores(st, 1.0f);
+            next_keys();
+            // chunk g's byte is held by the lanes with r16 / 4 = g
+            const float ks = e8m0_to_f32((uint32_t)__shfl((int)kb_now, 4 * g, 64)) * scale;
+            const int id = here.of(g);
+            float mx = kNone;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = t0 + 16 * g + 4 * t + e;
+                    const bool see = id >= 0 && key <= pos && key < rg.hi && (key > wlo || key < p.sinks);
+                    st[t][e] = see ? st[t][e] * ks : kNone;
+                    mx = fmaxf(mx, st[t][e]);
+                }
+            const float mu = follow(mx);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    // masked: below every probability, so that it can be told apart
+                    const bool see = st[t][e] != kNone;
+                    st[t][e] = see ? __builtin_amdgcn_exp2f(st[t][e] - mu) : -1.0f;
+                    l += see ? st[t][e] : 0.0f;
+                }
+        }
+        wait_values();
+        const float vs = e8m0_to_f32(vb);
+        if (whole && __builtin_amdgcn_ballot_w64(!plain_scale(vb)) == 0) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pf[t >> 1][4 * (t & 1) + e] = (__bf16)st[t][e];
+            add(std::false_type{}, pf, vs, 0);
+        } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    pf[t >> 1][4 * (t & 1) + e] = (__bf16)(st[t][e] == -1.0f ? 0.0f : st[t][e] * vs);
+            add(std::true_type{}, pf, 1.0f, seen16(rg, here.of(g), t0 + 16 * g));
+        }
+        wait_lds();           // the values' reads have returned
+        if (more) {
+            fetch_values(next, rg.start(i + WAVES));
+            here = next;
+            if (i + 2 * WAVES < b1) next = ids_of<SMALL>(c, table, rg.start(i + 2 * WAVES), rg.hi);
         }
     }
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
 
-    // the four waves' sums, joined in wave order
+    // the waves' sums, joined in wave order, in the keys' buffer
     __shared__ float wm[WAVES][ROWS], wl[WAVES][ROWS];
-    __shared__ v4f wo[WAVES][DT][64];
+    v4f *const wo = reinterpret_cast<v4f *>(keys);
+    static_assert(WAVES * DT * 64 * 16 <= WAVES * T::K_BYTES, "the sums fit");
+    wait_lds();
     if (g == 0) {
         wm[wave][r16] = m;
         wl[wave][r16] = l;
@@ -212,71 +278,97 @@ __global__ __launch_bounds__(THREADS, 2) void decode_kernel(AttnArgs p)
     for (int w = 0; w < WAVES; ++w) lt += wl[w][r16] * __builtin_amdgcn_exp2f(wm[w][r16] - mu);
     const float mine = __builtin_amdgcn_exp2f(m - mu);
 #pragma unroll
-    for (int d = 0; d < DT; ++d) wo[wave][d][lane] = o[d] * mine;
+    for (int d = 0; d < DT; ++d) wo[(wave * DT + d) * 64 + lane] = o[d] * mine;
     __syncthreads();
     const int64_t tile = (((int64_t)s * c.kv_heads + head) * p.row_tiles + rt) * p.splits + sp;
     float *const part = p.ws + tile * (ROWS * (D + 2));
 #pragma unroll
     for (int d = wave; d < DT; d += WAVES) {
-        v4f v = wo[0][d][lane];
+        v4f v = wo[d * 64 + lane];
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) v += wo[w][d][lane];
+        for (int w = 1; w < WAVES; ++w) v += wo[(w * DT + d) * 64 + lane];
         // column r16, rows (dims) 16 d + 4 g .. + 3
         if (p.splits > 1) {
-            *reinterpret_cast<v4f *>(part + r16 * D + 16 * d + 4 * g) = v;
+            if (live) *reinterpret_cast<v4f *>(part + r16 * D + 16 * d + 4 * g) = v;
         } else if (live) {
-            const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
-            v *= inv;
+            v *= lt == 0.0f ? 0.0f : 1.0f / lt;
             *reinterpret_cast<v2i *>(p.O + (q.q0 + qi) * p.o_stride + (int64_t)(head * G + qh) * D + 16 * d + 4 * g) =
                 v2i{(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3])};
         }
     }
     if (wave == 0 && g == 0) {
-        if (p.splits > 1) {
+        if (p.splits > 1) {   // rows past the sequence's are never joined
             part[ROWS * D + r16] = mt;
             part[ROWS * D + ROWS + r16] = lt;
         } else if (live && p.lse) {
-            p.lse[(q.q0 + qi) * p.q_heads + head * G + qh] = (mu + __builtin_log2f(lt)) * 0.6931471805599453f;
+            p.lse[(q.q0 + qi) * p.q_heads + head * G + qh] = (mu + __builtin_log2f(lt)) * kLn2;
         }
     }
 }
 
-// The splits' partial sums of one row tile, joined in split order.
+// The splits' partial sums of one row, joined in a fixed order: lane group q
+// of 256 / (D / 4) adds splits q, q + groups, ..., then the groups are added in
+// turn.  The weights 2^(m_k - m) of all splits are computed once, by one wave.
+constexpr int JOIN_THREADS = 256, MAX_SPLITS = 64;
 template <int D>
-__global__ __launch_bounds__(THREADS) void join_kernel(AttnArgs p)
+__global__ __launch_bounds__(JOIN_THREADS) void join_kernel(AttnArgs p)
 {
+    constexpr int LANES = D / 4, GROUPS = JOIN_THREADS / LANES;
+    constexpr int64_t PITCH = ROWS * (D + 2);
     const Pages &c = p.c;
-    int bid = blockIdx.x;
-    const int rt = bid % p.row_tiles;
+    const int r = blockIdx.x % ROWS;
+    const int64_t tile = blockIdx.x / ROWS;
+    int64_t bid = tile;
+    const int rt = (int)(bid % p.row_tiles);
     bid /= p.row_tiles;
-    const int head = bid % c.kv_heads, s = bid / c.kv_heads;
+    const int head = (int)(bid % c.kv_heads), s = (int)(bid / c.kv_heads);
     const Seq q = cache::sequence(c, s);
     const int G = p.group;
-    const int64_t rows = (int64_t)q.n * G, row0 = (int64_t)rt * ROWS;
-    if (row0 >= rows) return;
-    const float *const part = p.ws + (int64_t)blockIdx.x * p.splits * (ROWS * (D + 2));
-    constexpr int64_t PITCH = ROWS * (D + 2);
-    for (int i = threadIdx.x; i < ROWS * D / 4; i += THREADS) {
-        const int r = i / (D / 4), d = 4 * (i % (D / 4));
-        const int64_t row = row0 + r;
-        if (row >= rows) continue;
-        float mt = kNone;
-        for (int k = 0; k < p.splits; ++k) mt = fmaxf(mt, part[k * PITCH + ROWS * D + r]);
-        const float mu = mt == kNone ? 0.0f : mt;
-        float lt = 0.0f;
-        v4f v = {0.f, 0.f, 0.f, 0.f};
-        for (int k = 0; k < p.splits; ++k) {
-            const float f = __builtin_amdgcn_exp2f(part[k * PITCH + ROWS * D + r] - mu);
-            lt += part[k * PITCH + ROWS * D + ROWS + r] * f;
-            v += *reinterpret_cast<const v4f *>(part + k * PITCH + r * D + d) * f;
+    const int64_t row = (int64_t)rt * ROWS + r;
+    if (row >= (int64_t)q.n * G) return;
+    const float *const part = p.ws + tile * p.splits * PITCH;
+
+    __shared__ float weight[MAX_SPLITS], total[2];
+    __shared__ v4f sums[GROUPS][LANES];
+    const int tid = threadIdx.x;
+    if (tid < 64) {
+        float m = kNone, l = 0.0f;
+        if (tid < p.splits) {
+            m = part[tid * PITCH + ROWS * D + r];
+            l = part[tid * PITCH + ROWS * D + ROWS + r];
         }
-        v *= lt == 0.0f ? 0.0f : 1.0f / lt;
-        const int64_t token = q.q0 + row / G;
-        const int h = head * G + (int)(row % G);
-        *reinterpret_cast<v2i *>(p.O + token * p.o_stride + (int64_t)h * D + d) =
-            v2i{(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3])};
-        if (d == 0 && p.lse) p.lse[token * p.q_heads + h] = (mu + __builtin_log2f(lt)) * 0.6931471805599453f;
+        float mt = m;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) mt = fmaxf(mt, __shfl_xor(mt, d, 64));
+        const float mu = mt == kNone ? 0.0f : mt;
+        const float w = __builtin_amdgcn_exp2f(m - mu);
+        l *= w;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d, 64);
+        weight[tid] = w;
+        if (tid == 0) {
+            total[0] = mu;
+            total[1] = l;
+        }
     }
+    __syncthreads();
+    const int d4 = tid % LANES, g = tid / LANES;
+    v4f v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = g; k < p.splits; k += GROUPS)
+        v += *reinterpret_cast<const v4f *>(part + k * PITCH + r * D + 4 * d4) * weight[k];
+    sums[g][d4] = v;
+    __syncthreads();
+    if (g) return;
+#pragma unroll
+    for (int k = 1; k < GROUPS; ++k) v += sums[k][d4];
+    const float l = total[1];
+    v *= l == 0.0f ? 0.0f : 1.0f / l;
+    const int64_t token = q.q0 + row / G;
+    const int h = head * G + (int)(row % G);
+    *reinterpret_cast<v2i *>(p.O + token * p.o_stride + (int64_t)h * D + 4 * d4) =
+        v2i{(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3])};
+    if (tid == 0 && p.lse) p.lse[token * p.q_heads + h] = (total[0] + __builtin_log2f(l)) * kLn2;
 }
 
 } // namespace attn

@@ -32,7 +32,7 @@ struct AttnArgs {
     int64_t q_stride, o_stride;
     int q_heads, group;   // group = q_heads / kv_heads
     float scale_log2;     // softmax_scale * log2(e)
-    int64_t window, sinks;
+    int window, sinks;
     int row_tiles, splits;
     float *ws;            // split partials (splits > 1)
 };
@@ -76,5 +76,6 @@ hipError_t launch_attn_decode(int head_dim, const cache::AttnArgs &a, hipStream_
 
 // rows of one row tile of the decode kernel (queries times heads of a group)
 constexpr int kDecodeRows = 16;
+constexpr int kMaxSplits = 64;
 
 } // namespace mxg
