@@ -12,7 +12,7 @@ CSRC = os.path.join(HERE, "csrc")
 # (each holds that family's template instantiations), compiled in parallel
 SRCS = ["k_large_exact.hip", "k_large_exact_b.hip", "k_large_native.hip", "k_large_e2m1.hip",
         "k_stream.hip", "k_skinny_fp8.hip", "k_skinny_e2m1.hip", "k_quant.hip", "mxgemm.hip",
-        "k_block_small.hip", "k_block_native.hip", "k_block_exact.hip", "k_block_quant.hip", "k_cache.hip", "k_attn_decode.hip",
+        "k_block_small.hip", "k_block_native.hip", "k_block_exact.hip", "k_block_quant.hip", "k_cache.hip", "k_attn_decode.hip", "k_attn_prompt.hip",
         "mxblock.hip", "mxcache.hip"]
 OUT = os.path.join(HERE, "libmxgemm.so")
 ARCH = "gfx950"

@@ -1,0 +1,240 @@
+// mxattn_prompt.h -- attention over the 8-bit cache for many query rows
+// (prompts, entered whole or in pieces): MFMA- and VALU-bound.
+//
+// A workgroup of four waves takes 128 rows ((new token, query head of the
+// group) pairs, in token order), 32 a wave, and walks the visible keys in
+// blocks of 64, whose keys and values the waves load into one of two LDS
+// buffers together while the other is used: as codes, so that a read moves
+// half the bytes; each wave widens what it reads.  Per block a wave computes
+//   S^T = K Q^T, O^T += V^T P^T     32x32x16 bf16 MFMA
+// with a row in each MFMA column (lane l: row l % 32, lane half h = l / 32).
+// As in the decode kernel the softmax needs no exchange of data: the token
+// that MFMA row r of tile t (32 tokens) stands for is
+//   32 t + 16 (r / 4 % 2) + 8 (r / 16) + 4 (r / 8 % 2) + r % 4,
+// so that a lane's registers are the 16 tokens of chunk 2 t + h in order,
+// which is what it supplies to the second product, and 16 contiguous bytes of
+// each row of the values.  The chunk's scale bytes go into the widening.
+//
+// Blocks beyond a wave's own rows (causality, the window) are skipped by the
+// wave; whole blocks take a path without masks.  The running maximum lags as
+// in the decode kernel (rescaling 64 registers at every block otherwise).
+// The longest rows' workgroups start first.
+#pragma once
+
+#include "mxattn.h"
+
+#include <type_traits>
+
+namespace mxg {
+namespace attn_prompt {
+
+using namespace attn;
+
+constexpr int WAVES = 4, THREADS = 64 * WAVES, WAVE_ROWS = 32, ROWS = WAVES * WAVE_ROWS;
+
+template <int D, bool SMALL>
+__global__ __launch_bounds__(THREADS, 2) void kernel(AttnArgs p)
+{
+    constexpr int CH = D / 32;      // 16-byte key chunks per lane and token
+    constexpr int DT = D / 32;      // 32-row tiles of O^T
+    using T = Tile<D>;
+    __shared__ __attribute__((aligned(1024))) uint8_t buf0[T::BYTES], buf1[T::BYTES];
+    const Pages &c = p.c;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r32 = lane & 31, h = lane >> 5;
+    int64_t bid = blockIdx.x;
+    const int head = (int)(bid % c.kv_heads);
+    bid /= c.kv_heads;
+    const int s = (int)(bid % c.seqs);
+    const int rt = p.row_tiles - 1 - (int)(bid / c.seqs);
+
+    const Seq q = cache::sequence(c, s);
+    const int G = p.group;
+    const int64_t rows = (int64_t)q.n * G, row0 = (int64_t)rt * ROWS;
+    if (row0 >= rows) return;
+    const Range rg = range_of(p, q.ctx, position(q, row0 / G), position(q, (min(row0 + ROWS, rows) - 1) / G));
+    // this wave's rows
+    const int64_t w0 = row0 + wave * WAVE_ROWS;
+    const bool any = w0 < rows;
+    const int pmin = position(q, (any ? w0 : row0) / G);
+    const int pmax = position(q, (any ? min(w0 + WAVE_ROWS, rows) - 1 : row0) / G);
+    const int64_t row = w0 + r32;
+    const bool live = row < rows;
+    const int qi = (int)((live ? row : row0) / G), qh = (int)((live ? row : row0) % G);
+    const int pos = position(q, qi);
+    const int wlo = p.window ? pos - p.window : -0x7fffffff - 1;   // key > wlo is inside the window
+    const float scale = fabsf(p.scale_log2);
+
+    const uint32_t page1 = (uint32_t)D << c.shift, head_at = head * page1, page = page1 * c.kv_heads;
+    const int32_t *const table = c.table + (int64_t)s * c.max_pages;
+    auto fetch = [&](uint8_t *dst, const Ids<SMALL> &ids, int t0) MXG_INLINE {
+        T::template load_keys<WAVES>(c, ids, head_at, page, t0, wave, dst);
+        T::template load_values<WAVES>(c, ids, head_at, page, t0, wave, dst + T::K_BYTES);
+    };
+    Ids<SMALL> here = {}, next = {};
+    if (rg.count > 0) {
+        here = ids_of<SMALL>(c, table, rg.start(0), rg.hi);
+        fetch(buf0, here, rg.start(0));
+    }
+
+    v8bf qf[2 * CH];
+    {
+        const uint16_t *src = p.Q + (q.q0 + qi) * p.q_stride + (int64_t)(head * G + qh) * D;
+        const int flip = p.scale_log2 < 0.0f ? (int)0x80008000u : 0;
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                v4i x = *reinterpret_cast<const v4i *>(src + 16 * (2 * i + h) + 8 * u);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] ^= flip;
+                qf[2 * i + u] = __builtin_bit_cast(v8bf, x);
+            }
+    }
+    v16f o[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[d] = v16f{};
+    float m = kNone, l = 0.0f;
+    // token of MFMA row r32 in its tile, and that row's chunk
+    const int token = 16 * (r32 >> 2 & 1) + 8 * (r32 >> 4) + 4 * (r32 >> 3 & 1) + (r32 & 3);
+
+    auto block = [&](auto EDGE, const uint8_t *src, const Ids<SMALL> &ids, int t0, const uint32_t (&kb)[2],
+                     const uint32_t (&vb)[2]) MXG_INLINE {
+        constexpr bool edge = decltype(EDGE)::value;
+        v16f st[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            // kb, vb are of the lane's own chunk 2t + h; the key row r32 lies in
+            // chunk 2t + (r32 / 4 % 2)
+            float ks = 1.0f;
+            if constexpr (!edge)
+                ks = e8m0_to_f32(SMALL ? (uint32_t)__shfl((int)kb[t], 32 * (r32 >> 2 & 1), 64) : kb[t]);
+            st[t] = v16f{};
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                v8bf lo, hi;
+                decode16<0>(*reinterpret_cast<const v4i *>(src + T::key(32 * t + token, 2 * i + h)), ks, lo, hi);
+                st[t] = mfma_bf16_32(lo, qf[2 * i], st[t]);
+                st[t] = mfma_bf16_32(hi, qf[2 * i + 1], st[t]);
+            }
+        }
+        float mx = kNone;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int key0 = t0 + 32 * t + 16 * h;
+            const int id = edge ? ids.of(2 * t + h) : 0;
+            const float ks = edge ? e8m0_to_f32(kb[t]) * scale : 1.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                if constexpr (edge) {
+                    const int key = key0 + e;
+                    const bool see = id >= 0 && key <= pos && key < rg.hi && (key > wlo || key < p.sinks);
+                    st[t][e] = see ? st[t][e] * ks : kNone;
+                }
+                mx = fmaxf(mx, st[t][e]);   // a NaN score passes by: it makes the row's sum NaN
+            }
+        }
+        if constexpr (!edge) mx *= scale;
+        {
+            const uint32_t b = __builtin_bit_cast(uint32_t, mx);
+            const auto u = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+            const uint32_t u0 = u[0], u1 = u[1];
+            mx = fmaxf(__builtin_bit_cast(float, u0), __builtin_bit_cast(float, u1));
+        }
+        if (__builtin_amdgcn_ballot_w64(mx > m + 8.0f)) {
+            const float mn = fmaxf(m, mx), alpha = mn == kNone ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+            m = mn;
+            l *= alpha;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[d] *= alpha;
+        }
+        const float mu = m == kNone ? 0.0f : m;
+        v8bf pf[2][2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const float vs = edge ? e8m0_to_f32(vb[t]) : 1.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                float x;
+                if constexpr (edge) {
+                    const bool see = st[t][e] != kNone;
+                    x = see ? __builtin_amdgcn_exp2f(st[t][e] - mu) : 0.0f;
+                    l += x;
+                    x = see ? x * vs : 0.0f;
+                } else {
+                    x = __builtin_amdgcn_exp2f(__builtin_fmaf(st[t][e], scale, -mu));
+                    l += x;
+                }
+                pf[t][e >> 3][e & 7] = (__bf16)x;
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const float vs = edge ? 1.0f : e8m0_to_f32(vb[t]);
+            const uint32_t keep = edge ? seen16(rg, ids.of(2 * t + h), t0 + 32 * t + 16 * h) : 0;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                v4i x = *reinterpret_cast<const v4i *>(src + T::K_BYTES + T::value(32 * d + r32, 2 * t + h));
+                if constexpr (edge) x = keep16(x, keep);
+                v8bf lo, hi;
+                decode16<0>(x, vs, lo, hi);
+                o[d] = mfma_bf16_32(lo, pf[t][0], o[d]);
+                o[d] = mfma_bf16_32(hi, pf[t][1], o[d]);
+            }
+        }
+    };
+
+    auto step = [&](int i, const uint8_t *src, uint8_t *other) MXG_INLINE {
+        const int t0 = rg.start(i);
+        // scale bytes of this lane's chunks
+        uint32_t kb[2], vb[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const size_t at = (size_t)max(here.of(2 * t + h), 0) * c.kv_heads + head;
+            kb[t] = c.ks[at];
+            vb[t] = c.vs[at];
+        }
+        // the block has landed for every wave, and the other buffer is read out
+        wait_vmem();
+        __syncthreads();
+        if (i + 1 < rg.count) {
+            next = ids_of<SMALL>(c, table, rg.start(i + 1), rg.hi);
+            fetch(other, next, rg.start(i + 1));
+        }
+        // a wave that sees nothing of the block has no part in it
+        const bool seen = any && t0 <= pmax && (!p.window || t0 + BLOCK - 1 > pmin - p.window || t0 < p.sinks);
+        if (seen) {
+            const bool odd = !plain_scale(kb[0]) || !plain_scale(kb[1]) || !plain_scale(vb[0]) || !plain_scale(vb[1]);
+            const bool whole = here.all() && t0 + BLOCK <= rg.hi && t0 + BLOCK - 1 <= pmin &&
+                               (!p.window || t0 > pmax - p.window) && __builtin_amdgcn_ballot_w64(odd) == 0;
+            if (whole)
+                block(std::false_type{}, src, here, t0, kb, vb);
+            else
+                block(std::true_type{}, src, here, t0, kb, vb);
+        }
+        here = next;
+    };
+    for (int i = 0; i < rg.count; i += 2) {
+        step(i, buf0, buf1);
+        if (i + 1 < rg.count) step(i + 1, buf1, buf0);
+    }
+
+    l += __shfl_xor(l, 32, 64);
+    if (!live) return;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    // column r32, rows (dims) 32 d + 8 e + 4 h .. + 3
+    uint16_t *const dst = p.O + (q.q0 + qi) * p.o_stride + (int64_t)(head * G + qh) * D;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float x0 = o[d][4 * e] * inv, x1 = o[d][4 * e + 1] * inv, x2 = o[d][4 * e + 2] * inv,
+                        x3 = o[d][4 * e + 3] * inv;
+            *reinterpret_cast<v2i *>(dst + 32 * d + 8 * e + 4 * h) = v2i{(int)pack_bf16x2(x0, x1), (int)pack_bf16x2(x2, x3)};
+        }
+    if (h == 0 && p.lse)
+        p.lse[(q.q0 + qi) * p.q_heads + head * G + qh] = ((m == kNone ? 0.0f : m) + __builtin_log2f(l)) * kLn2;
+}
+
+} // namespace attn_prompt
+} // namespace mxg

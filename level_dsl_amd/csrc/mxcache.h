@@ -74,6 +74,10 @@ __device__ __forceinline__ int page_of(const Pages &c, int s, int index)
 hipError_t launch_cache_append(int x_bf16, int head_dim, const cache::AppendArgs &a, hipStream_t s);  // k_cache.hip
 hipError_t launch_attn_decode(int head_dim, const cache::AttnArgs &a, hipStream_t s);                  // k_attn_decode.hip
 
+hipError_t launch_attn_prompt(int head_dim, const cache::AttnArgs &a, hipStream_t s);                  // k_attn_prompt.hip
+
+// rows of one row tile of the prompt kernel
+constexpr int kPromptRows = 128;
 // rows of one row tile of the decode kernel (queries times heads of a group)
 constexpr int kDecodeRows = 16;
 constexpr int kMaxSplits = 64;

@@ -90,12 +90,20 @@ int64_t row_tiles(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads)
     return (rows + mxg::kDecodeRows - 1) / mxg::kDecodeRows;
 }
 
+// The prompt kernel, or the decode kernel, which reads the keys once for every
+// 16 rows.
+bool use_prompt(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads)
+{
+    return std::min(b->max_q, b->rows) * (q_heads / c->kv_heads) > 32;
+}
+
 // Splits of the visible keys: enough workgroups for two on each of the 256
 // CUs, but at least four 64-key blocks (one per wave) a split.  More of them cost
 // more than their balance gains (64 sequences of 4097 to 8192 tokens, 8 kv
 // heads: 1 split 160 us, 2: 176, 4: 173).
 int choose_splits(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads, int64_t window)
 {
+    if (use_prompt(c, b, q_heads)) return 1;
     const int64_t tiles = b->seqs * c->kv_heads * row_tiles(c, b, q_heads);
     const int64_t reach = std::min(b->max_ctx, b->max_pages * c->page_size);
     const int64_t keys = window ? std::min(reach, window + std::min(b->max_q, b->rows)) : reach;
@@ -237,7 +245,9 @@ int mxgemm_cache_attention(mxgemm_t h, const mxgemm_cache *cache, const mxgemm_b
     a.row_tiles = (int)row_tiles(cache, batch, q_heads);
     a.splits = ws ? choose_splits(cache, batch, q_heads, window) : 1;
     a.ws = (float *)ws;
-    return mxg::launch_attn_decode(cache->head_dim, a, stream) == hipSuccess ? MXGEMM_OK : MXGEMM_ERR_HIP;
+    const hipError_t e = use_prompt(cache, batch, q_heads) ? mxg::launch_attn_prompt(cache->head_dim, a, stream)
+                                                           : mxg::launch_attn_decode(cache->head_dim, a, stream);
+    return e == hipSuccess ? MXGEMM_OK : MXGEMM_ERR_HIP;
 }
 
 } // extern "C"
