@@ -155,9 +155,17 @@ def mxgemm_set_variant(h: int, variant: int) -> None:
     _check(load_library().mxgemm_set_variant(h, int(variant)), "mxgemm_set_variant")
 
 
+# the current stream's handle without a Stream object around it (2.7 us less
+# a call), where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None or _current_device is None or not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_current_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -509,25 +517,26 @@ class Gemm:
         (M, K) and B (N, K) with fp32 scales A_scale (M, ceil(K / 128)) and
         B_scale (ceil(N / 128), ceil(K / 128)), or (N, ceil(K / 128)) for one
         scale per row; C (M, N) float32 or bfloat16."""
-        if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
+        if A.dim() != 2 or B.dim() != 2:
             raise ValueError("A must be (M, K) and B (N, K)")
-        (M, K), N = A.shape, B.shape[0]
+        (M, K), (N, kB) = A.shape, B.shape
         kb, nb = (K + 127) // 128, (N + 127) // 128
-        if A_scale.shape != (M, kb) or B_scale.shape not in ((nb, kb), (N, kb)):
-            raise ValueError("A_scale must be (M, ceil(K / 128)) and B_scale (ceil(N / 128), "
-                             "ceil(K / 128)) or (N, ceil(K / 128))")
-        if C.shape != (M, N) or C.dtype not in (torch.float32, torch.bfloat16):
+        sb = B_scale.shape
+        if kB != K or A_scale.shape != (M, kb) or (sb != (nb, kb) and sb != (N, kb)):
+            raise ValueError("A must be (M, K), B (N, K), A_scale (M, ceil(K / 128)) and B_scale "
+                             "(ceil(N / 128), ceil(K / 128)) or (N, ceil(K / 128))")
+        f32 = C.dtype == torch.float32
+        if C.shape != (M, N) or not (f32 or C.dtype == torch.bfloat16):
             raise ValueError(f"C must be ({M}, {N}) float32 or bfloat16")
         if A.dtype != torch.uint8 or B.dtype != torch.uint8 or A_scale.dtype != torch.float32 or \
                 B_scale.dtype != torch.float32:
             raise ValueError("codes must be uint8 and scales float32")
         _same_device(A, A_scale, B, B_scale, C)
-        for t in (A, A_scale, B, B_scale, C):
-            if not t.is_contiguous():
-                raise ValueError("all operands must be contiguous")
-        mxgemm_run_block128(self.h, A, A_scale, fmtA, B, B_scale, fmtB,
-                            128 if B_scale.shape[0] == nb else 1, C, M, N, K, int(bool(use_acc)),
-                            MXGEMM_OUT_F32 if C.dtype == torch.float32 else MXGEMM_OUT_BF16, stream)
+        if not (A.is_contiguous() and B.is_contiguous() and A_scale.is_contiguous() and
+                B_scale.is_contiguous() and C.is_contiguous()):
+            raise ValueError("all operands must be contiguous")
+        mxgemm_run_block128(self.h, A, A_scale, fmtA, B, B_scale, fmtB, 128 if sb[0] == nb else 1, C,
+                            M, N, K, use_acc, MXGEMM_OUT_F32 if f32 else MXGEMM_OUT_BF16, stream)
         return C
 
     def quantize_block128(self, X, fmt, rows=1, normal=True, transposed=False, stream=None):
@@ -545,32 +554,34 @@ class Gemm:
             raise ValueError("nothing to compute: normal and transposed are both off")
         R, K = X.shape
         kb, rb = (K + 127) // 128, (R + 127) // 128
-        out = []
+        dev, c, sc, ct, st = X.device, None, None, None, None
         with _on_stream(stream):
             if normal:
-                out += [torch.empty((R, K), dtype=torch.uint8, device=X.device),
-                        torch.empty((R if rows == 1 else rb, kb), dtype=torch.float32, device=X.device)]
+                c = torch.empty((R, K), dtype=torch.uint8, device=dev)
+                sc = torch.empty((R if rows == 1 else rb, kb), dtype=torch.float32, device=dev)
             if transposed:
-                out += [torch.empty((K, (R + 15) // 16 * 16), dtype=torch.uint8, device=X.device),
-                        torch.empty((K if rows == 1 else kb, rb), dtype=torch.float32, device=X.device)]
-        c, s = out[:2] if normal else (None, None)
-        ct, st = out[-2:] if transposed else (None, None)
+                ct = torch.empty((K, (R + 15) // 16 * 16), dtype=torch.uint8, device=dev)
+                st = torch.empty((K if rows == 1 else kb, rb), dtype=torch.float32, device=dev)
         mxgemm_quantize_block128(self.h, X, MXGEMM_X_F32 if X.dtype == torch.float32 else MXGEMM_X_BF16,
-                                 R, K, rows, fmt, c, s, ct, st, stream)
-        return tuple(out)
+                                 R, K, rows, fmt, c, sc, ct, st, stream)
+        return (c, sc) if not transposed else (c, sc, ct, st) if normal else (ct, st)
 
 
 def _same_device(*tensors):
-    d = tensors[0].device
-    if d.type != "cuda" or any(t.device != d for t in tensors):
-        raise ValueError("all tensors must be on one GPU")
+    d = tensors[0].get_device()     # -1 on the host
+    for t in tensors:
+        if t.get_device() != d or d < 0:
+            raise ValueError("all tensors must be on one GPU")
+
+
+_NOTHING = contextlib.nullcontext()
 
 
 def _on_stream(stream):
     """The context in which a call on `stream` allocates, so that the memory
     is not handed out again before that stream is done with it."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _NOTHING
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream)
     return torch.cuda.stream(stream)
@@ -601,15 +612,24 @@ class Batch:
             if t.dtype != torch.int32 or not t.is_contiguous():
                 raise ValueError("page_table, q_start and ctx_len must be contiguous int32")
         self.tensors = (page_table, q_start, ctx_len)   # kept alive
-        self.max_q, self.max_ctx = int(max_q), max_ctx
+        self.max_q, self.max_ctx = int(max_q), None if max_ctx is None else int(max_ctx)
+        self.device = page_table.get_device()
+        self._structs = {}
 
     def struct(self, cache, rows: int) -> BatchStruct:
-        t, q, c = self.tensors
-        if t.device != cache.device:
+        """The mxgemm_batch of a call on `rows` tokens over `cache`."""
+        key = (rows, cache.page_size)
+        got = self._structs.get(key)
+        if got is None:
+            t, q, c = self.tensors
+            reach = t.shape[1] * cache.page_size
+            got = BatchStruct(t.data_ptr(), q.data_ptr(), c.data_ptr(), t.shape[0], t.shape[1], rows,
+                              self.max_q, reach if self.max_ctx is None else self.max_ctx)
+            if len(self._structs) < 64:
+                self._structs[key] = got
+        if self.device != cache.device:
             raise ValueError("the batch and the cache must be on one GPU")
-        reach = t.shape[1] * cache.page_size
-        return BatchStruct(t.data_ptr(), q.data_ptr(), c.data_ptr(), t.shape[0], t.shape[1], rows,
-                           self.max_q, reach if self.max_ctx is None else int(self.max_ctx))
+        return got
 
 
 class KVCache:
@@ -632,7 +652,7 @@ class KVCache:
         for t in self.tensors:
             if t.dtype != torch.uint8 or not t.is_contiguous():
                 raise ValueError("codes and scales must be contiguous uint8")
-        self.gemm, self.device = gemm, k_codes.device
+        self.gemm, self.device = gemm, k_codes.get_device()
         self.page_size, self.kv_heads, self.head_dim = page, heads, dim
         self.struct = CacheStruct(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                                   v_scales.data_ptr(), pages, page, heads, dim)
@@ -654,7 +674,7 @@ class KVCache:
             raise ValueError("V must match K in shape, type and stride")
         if K.dtype not in (torch.float32, torch.bfloat16):
             raise ValueError("K and V must be float32 or bfloat16")
-        if K.device != self.device or V.device != self.device:
+        if K.get_device() != self.device or V.get_device() != self.device:
             raise ValueError("K, V and the cache must be on one GPU")
         if K.shape[0] == 0:
             return
@@ -669,20 +689,23 @@ class KVCache:
         head_dim ** -0.5; window > 0 hides keys that far back or further,
         except the first `sinks`.  Rows of out outside every sequence are not
         written."""
-        if Q.dim() != 3 or Q.dtype != torch.bfloat16 or Q.device != self.device:
+        if Q.dim() != 3 or Q.dtype != torch.bfloat16 or Q.get_device() != self.device:
             raise ValueError("Q must be a (tokens, q_heads, head_dim) bfloat16 tensor on the cache's GPU")
         T, heads, dim = Q.shape
         q_stride = _token_stride(Q, heads, self.head_dim, "Q")
         with _on_stream(stream):
             if out is None:
                 out = torch.empty((T, heads, dim), dtype=torch.bfloat16, device=Q.device)
+                o_stride = heads * dim
+            else:
+                if out.shape != Q.shape or out.dtype != torch.bfloat16 or out.get_device() != self.device:
+                    raise ValueError("out must be bfloat16 like Q")
+                o_stride = _token_stride(out, heads, dim, "out")
             if lse is None:
                 lse = torch.empty((T, heads), dtype=torch.float32, device=Q.device)
-            if out.shape != Q.shape or out.dtype != torch.bfloat16 or out.device != self.device or \
-                    lse.shape != (T, heads) or lse.dtype != torch.float32 or lse.device != self.device or \
+            elif lse.shape != (T, heads) or lse.dtype != torch.float32 or lse.get_device() != self.device or \
                     not lse.is_contiguous():
-                raise ValueError("out must be bfloat16 like Q, lse a contiguous (tokens, q_heads) float32")
-            o_stride = _token_stride(out, heads, dim, "out")
+                raise ValueError("lse must be a contiguous (tokens, q_heads) float32")
             if T == 0:
                 return out, lse
             b = batch.struct(self, T)
