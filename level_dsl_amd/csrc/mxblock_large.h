@@ -41,6 +41,15 @@ constexpr int BM = 256, BK = 128, MT = 4;
 template <bool NATIVE>
 constexpr int columns() { return NATIVE ? 256 : 128; }
 
+// Workgroup barrier behind this wave's LDS reads and writes, but not its
+// direct-to-LDS loads, whose landing it waits for by count.
+__device__ __forceinline__ void barrier_lds()
+{
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    barrier_nofence();
+}
+
 // One 16x16x128 fp8 MFMA without block scales.
 template <int FX, int FY>
 __device__ __forceinline__ v4f mfma_f8_16(v8i x, v8i y, v4f c)
@@ -54,9 +63,8 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(block::Args p)
     constexpr int BN = columns<NATIVE>(), NT = BN / 32;   // column tiles of a wave
     constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK;
     constexpr int A_SEGS = A_BYTES / 1024 / WAVES, B_SEGS = B_BYTES / 1024 / WAVES;
-    // separate objects, so that a read of one does not wait for loads into the other
-    __shared__ __attribute__((aligned(1024))) uint8_t lds0[A_BYTES + B_BYTES];
-    __shared__ __attribute__((aligned(1024))) uint8_t lds1[A_BYTES + B_BYTES];
+    // separate objects, so that a read of one does not wait for loads into another
+    __shared__ __attribute__((aligned(1024))) uint8_t a0[A_BYTES], a1[A_BYTES], b0[B_BYTES], b1[B_BYTES];
     __shared__ float scale_a[2][4][BM];
     __shared__ float scale_b[ROWS_B == 1 ? 2 : 1][ROWS_B == 1 ? 4 : 1][ROWS_B == 1 ? BN : 1];
 
@@ -81,17 +89,16 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(block::Args p)
     // segment s holds tile rows 8s .. 8s+7; lane i writes row 8s + i/8 at chunk
     // position i % 8, i.e. global chunk (i % 8) ^ (i / 8)
     const uint32_t chunk = ((lane & 7) ^ (lane >> 3)) * 16;
-    const uint32_t rowA = (uint32_t)(8 * A_SEGS * wave + (lane >> 3)) * K;
-    const uint32_t rowB = (uint32_t)(8 * B_SEGS * wave + (lane >> 3)) * K;
-    auto gload = [&](uint8_t *buf, int kt) MXG_INLINE {
-        const uint32_t k = (uint32_t)kt * BK + chunk;
-        const bool in = (int)k < K;
-#pragma unroll
-        for (int j = 0; j < A_SEGS; ++j)
-            load16_lds(rA, buf + (A_SEGS * wave + j) * 1024, in ? rowA + (uint32_t)(8 * j) * K + k : kOob);
-#pragma unroll
-        for (int j = 0; j < B_SEGS; ++j)
-            load16_lds(rB, buf + A_BYTES + (B_SEGS * wave + j) * 1024, in ? rowB + (uint32_t)(8 * j) * K + k : kOob);
+    const uint32_t offA = (uint32_t)(8 * A_SEGS * wave + (lane >> 3)) * K + chunk;
+    const uint32_t offB = (uint32_t)(8 * B_SEGS * wave + (lane >> 3)) * K + chunk;
+    // load j of this wave's of stage kt (past K: zeros)
+    auto load_a = [&](uint8_t *buf, int kt, int j) MXG_INLINE {
+        load16_lds(rA, buf + (A_SEGS * wave + j) * 1024, kt * BK + (int)chunk < K ? offA : kOob,
+                   (uint32_t)(8 * j) * K + (uint32_t)kt * BK);
+    };
+    auto load_b = [&](uint8_t *buf, int kt, int j) MXG_INLINE {
+        load16_lds(rB, buf + (B_SEGS * wave + j) * 1024, kt * BK + (int)chunk < K ? offB : kOob,
+                   (uint32_t)(8 * j) * K + (uint32_t)kt * BK);
     };
     // scale windows: thread t < 256 a row of As, thread 256 + t a row of Bs
     // (ROWS_B == 1).  Values past a row's end are of stages that do not exist.
@@ -119,9 +126,10 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(block::Args p)
 
     const int sw = r16 & 7;
     const uint32_t o0 = (uint32_t)((g ^ sw) << 4), o1 = (uint32_t)(((4 + g) ^ sw) << 4);
-    const uint32_t fa_off = (uint32_t)(wm * 64 + r16) * BK, fb_off = (uint32_t)(A_BYTES + (wn * 16 * NT + r16) * BK);
+    const uint32_t fa_off = (uint32_t)(wm * 64 + r16) * BK, fb_off = (uint32_t)(wn * 16 * NT + r16) * BK;
 
-    auto compute = [&](const uint8_t *buf, int kt, float sb) MXG_INLINE {
+    // step: called in each column tile's step for the loads that go there
+    auto compute = [&](const uint8_t *la, const uint8_t *lb, int kt, float sb, auto &&step) MXG_INLINE {
         const int w = (kt >> 2) & 1, e4 = kt & 3;
         float s[MT];
 #pragma unroll
@@ -130,9 +138,9 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(block::Args p)
 #pragma unroll
             for (int i = 0; i < MT; ++i) s[i] *= sb;
         }
-        auto read = [&](uint32_t off) MXG_INLINE {
-            const v4i lo = *reinterpret_cast<const v4i *>(buf + off + o0);
-            const v4i hi = *reinterpret_cast<const v4i *>(buf + off + o1);
+        auto read = [&](const uint8_t *src) MXG_INLINE {
+            const v4i lo = *reinterpret_cast<const v4i *>(src + o0);
+            const v4i hi = *reinterpret_cast<const v4i *>(src + o1);
             return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         };
         auto join = [&](int j, const v4f (&t)[MT]) MXG_INLINE {
@@ -160,20 +168,22 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(block::Args p)
         // spills their sums.
         v4f t[2][MT];
         v8i b[2];
-        b[0] = read(fb_off);
+        b[0] = read(lb + fb_off);
         if constexpr (NATIVE) {
             v8i a[MT];
 #pragma unroll
-            for (int i = 0; i < MT; ++i) a[i] = read(fa_off + i * 16 * BK);
+            for (int i = 0; i < MT; ++i) a[i] = read(la + fa_off + i * 16 * BK);
             static_for<NT>([&](auto J) MXG_INLINE {
                 constexpr int j = decltype(J)::value;
-                if constexpr (j + 1 < NT) b[(j + 1) & 1] = read(fb_off + (j + 1) * 16 * BK);
+                if constexpr (j + 1 < NT) b[(j + 1) & 1] = read(lb + fb_off + (j + 1) * 16 * BK);
+                step(J);
 #pragma unroll
                 for (int i = 0; i < MT; ++i) t[j & 1][i] = mfma_f8_16<FB, FA>(b[j & 1], a[i], zero);
                 if constexpr (j > 0) join(j - 1, t[(j - 1) & 1]);
                 __builtin_amdgcn_sched_group_barrier(large::SG_DS_RD, 2, 0);
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
+                    if (i == 1) __builtin_amdgcn_sched_group_barrier(large::SG_VMEM_RD, 1, 0);
                     __builtin_amdgcn_sched_group_barrier(large::SG_MFMA, 1, 0);
                     __builtin_amdgcn_sched_group_barrier(large::SG_VALU, ROWS_B == 1 ? 8 : 4, 0);
                 }
@@ -183,7 +193,7 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(block::Args p)
             v8bf fa[MT][4];
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-                const v8i x = read(fa_off + i * 16 * BK);
+                const v8i x = read(la + fa_off + i * 16 * BK);
                 decode16<FA>(v4i{x[0], x[1], x[2], x[3]}, 1.0f, fa[i][0], fa[i][1]);
                 decode16<FA>(v4i{x[4], x[5], x[6], x[7]}, 1.0f, fa[i][2], fa[i][3]);
             }
@@ -192,7 +202,8 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(block::Args p)
                 constexpr int j = decltype(J)::value;
                 v8bf fb[4];
                 const v8i x = b[j & 1];
-                if constexpr (j + 1 < NT) b[(j + 1) & 1] = read(fb_off + (j + 1) * 16 * BK);
+                if constexpr (j + 1 < NT) b[(j + 1) & 1] = read(lb + fb_off + (j + 1) * 16 * BK);
+                step(J);
                 decode16<FB>(v4i{x[0], x[1], x[2], x[3]}, 1.0f, fb[0], fb[1]);
                 decode16<FB>(v4i{x[4], x[5], x[6], x[7]}, 1.0f, fb[2], fb[3]);
 #pragma unroll
@@ -209,32 +220,55 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(block::Args p)
     };
 
     // ---- main loop ----------------------------------------------------------
-    gload(lds0, 0);
-    v4i win = wload(0);
-    wstore(0, win);
+    // Stage kt's first half loads B of stage kt + 1, a load a step (a burst of
+    // them backs up the address path and stalls the waves behind it).  By its
+    // middle every wave holds its A rows in registers, so after a barrier
+    // there the second half loads A of stage kt + 2 over stage kt's.
     auto sb_of = [&](int kt) MXG_INLINE -> float {
         if constexpr (ROWS_B == 1) return 0.0f;
         return scalar_load(bs + min(kt, KB - 1));
     };
+#pragma unroll
+    for (int j = 0; j < A_SEGS; ++j) load_a(a0, 0, j);
+#pragma unroll
+    for (int j = 0; j < B_SEGS; ++j) load_b(b0, 0, j);
+    v4i win = wload(0);
+    wstore(0, win);
+#pragma unroll
+    for (int j = 0; j < A_SEGS; ++j) load_a(a1, 1, j);
     float sb = sb_of(0);
-    wait_vmem();
-    __syncthreads();
-    auto stage = [&](int kt, uint8_t *buf, uint8_t *other) MXG_INLINE {
-        gload(other, kt + 1);                       // past K: zeros, never read
-        if ((kt & 3) == 0) win = wload(kt + 4);
+    wait_vmcnt<A_SEGS>();
+    barrier_lds();
+    constexpr int HALF = NT / 2;               // steps before the middle
+    constexpr int A_STEP = A_SEGS / HALF, B_STEP = B_SEGS / HALF;
+    static_assert(A_STEP * HALF == A_SEGS && B_STEP * HALF == B_SEGS, "the loads divide over the steps");
+    auto stage = [&](int kt, auto PH) MXG_INLINE {   // PH = kt % 4
+        constexpr int ph = decltype(PH)::value;
+        uint8_t *const la = ph & 1 ? a1 : a0, *const lb = ph & 1 ? b1 : b0, *const other_b = ph & 1 ? b0 : b1;
+        if constexpr (ph == 0) win = wload(kt + 4);
         const float sb1 = sb_of(kt + 1);
-        compute(buf, kt, sb);
-        if ((kt & 3) == 3) wstore(((kt >> 2) + 1) & 1, win);
+        compute(la, lb, kt, sb, [&](auto J) MXG_INLINE {
+            constexpr int j = decltype(J)::value;
+            if constexpr (j < HALF) {
+#pragma unroll
+                for (int x = 0; x < B_STEP; ++x) load_b(other_b, kt + 1, j * B_STEP + x);
+            } else {
+                if constexpr (j == HALF) barrier_nofence();
+#pragma unroll
+                for (int x = 0; x < A_STEP; ++x) load_a(la, kt + 2, (j - HALF) * A_STEP + x);
+            }
+        });
+        if constexpr (ph == 3) wstore(((kt >> 2) + 1) & 1, win);
         sb = sb1;
-        wait_vmem();
-        __syncthreads();
+        wait_vmcnt<A_SEGS>();                  // all but A of stage kt + 2
+        barrier_lds();
     };
-    int kt = 0;
-    for (; kt + 2 <= KB; kt += 2) {
-        stage(kt, lds0, lds1);
-        stage(kt + 1, lds1, lds0);
+    for (int kt = 0; kt < KB; kt += 4) {
+        stage(kt, int_c<0>{});
+        if (kt + 1 < KB) stage(kt + 1, int_c<1>{});
+        if (kt + 2 < KB) stage(kt + 2, int_c<2>{});
+        if (kt + 3 < KB) stage(kt + 3, int_c<3>{});
     }
-    if (kt < KB) stage(kt, lds0, lds1);
 
     // ---- epilogue -------------------------------------------------------------
     const int esz = p.out_bf16 ? 2 : 4;

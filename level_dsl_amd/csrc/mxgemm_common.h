@@ -106,6 +106,12 @@ __device__ __forceinline__ void load16_lds(rsrc_t r, void *lds_base, uint32_t of
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)lds_base, 16, off, 0, 0, 0);
 }
 
+// The same with a wave-uniform part of the offset (range-checked together).
+__device__ __forceinline__ void load16_lds(rsrc_t r, void *lds_base, uint32_t off, uint32_t uniform)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)lds_base, 16, off, uniform, 0, 0);
+}
+
 // x itself, hidden from the optimizer's reassociation of address arithmetic
 // (an empty asm statement: no instruction is emitted).  v: a per-lane
 // value, s: a wave-uniform one.
