@@ -128,6 +128,7 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(block::Args p)
     const uint32_t o0 = (uint32_t)((g ^ sw) << 4), o1 = (uint32_t)(((4 + g) ^ sw) << 4);
     const uint32_t fa_off = (uint32_t)(wm * 64 + r16) * BK, fb_off = (uint32_t)(wn * 16 * NT + r16) * BK;
 
+    const uint32_t sn_off = opaque_v((uint32_t)(wn * 16 * NT + 4 * g) * 4);
     // step: called in each column tile's step for the loads that go there
     auto compute = [&](const uint8_t *la, const uint8_t *lb, int kt, float sb, auto &&step) MXG_INLINE {
         const int w = (kt >> 2) & 1, e4 = kt & 3;
@@ -143,13 +144,23 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(block::Args p)
             const v4i hi = *reinterpret_cast<const v4i *>(src + o1);
             return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         };
+        // B's scales of column tile j, read a step before they are used.  The
+        // address is the object plus two whole offsets: a longer chain loses
+        // the compiler's record of which object is read, and it would wait
+        // for the loads into the others.
+        v4f sn[2];
+        const uint32_t stage_off = opaque_s((uint32_t)(w * 4 + e4) * BN * 4);
+        auto read_sn = [&](int j) MXG_INLINE {
+            if constexpr (ROWS_B == 1)
+                sn[j & 1] = *reinterpret_cast<const v4f *>(reinterpret_cast<const uint8_t *>(scale_b) + stage_off + sn_off +
+                                                           j * 64);
+        };
         auto join = [&](int j, const v4f (&t)[MT]) MXG_INLINE {
             if constexpr (ROWS_B == 1) {
-                const v4f sn = *reinterpret_cast<const v4f *>(&scale_b[w][e4][wn * 16 * NT + 16 * j + 4 * g]);
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[i][j][e] += t[i][e] * s[i] * sn[e];
+                    for (int e = 0; e < 4; ++e) acc[i][j][e] += t[i][e] * s[i] * sn[j & 1][e];
             } else {
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
@@ -176,11 +187,12 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(block::Args p)
             static_for<NT>([&](auto J) MXG_INLINE {
                 constexpr int j = decltype(J)::value;
                 if constexpr (j + 1 < NT) b[(j + 1) & 1] = read(lb + fb_off + (j + 1) * 16 * BK);
+                read_sn(j);
                 step(J);
 #pragma unroll
                 for (int i = 0; i < MT; ++i) t[j & 1][i] = mfma_f8_16<FB, FA>(b[j & 1], a[i], zero);
                 if constexpr (j > 0) join(j - 1, t[(j - 1) & 1]);
-                __builtin_amdgcn_sched_group_barrier(large::SG_DS_RD, 2, 0);
+                __builtin_amdgcn_sched_group_barrier(large::SG_DS_RD, ROWS_B == 1 ? 3 : 2, 0);
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                     if (i == 1) __builtin_amdgcn_sched_group_barrier(large::SG_VMEM_RD, 1, 0);
@@ -203,6 +215,7 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(block::Args p)
                 v8bf fb[4];
                 const v8i x = b[j & 1];
                 if constexpr (j + 1 < NT) b[(j + 1) & 1] = read(lb + fb_off + (j + 1) * 16 * BK);
+                read_sn(j);
                 step(J);
                 decode16<FB>(v4i{x[0], x[1], x[2], x[3]}, 1.0f, fb[0], fb[1]);
                 decode16<FB>(v4i{x[4], x[5], x[6], x[7]}, 1.0f, fb[2], fb[3]);
