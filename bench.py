@@ -74,7 +74,7 @@ KERNEL_SOURCES = ["level_dsl_amd/csrc/" + f for f in (
     "k_large_exact_b.hip", "k_large_native.hip", "k_large_e2m1.hip", "k_stream.hip", "k_skinny_fp8.hip",
     "k_skinny_e2m1.hip", "k_quant.hip", "mxcopy.h", "mxwiden.h", "mxgemm_ctx.h", "mxblock.h",
     "mxblock.hip", "mxblock_small.h", "mxblock_large.h", "k_block_native.hip", "k_block_exact.hip", "mxblock_quant.h", "k_block_small.hip", "k_block_quant.hip",
-    "mxcache.h", "mxcache.hip", "mxcache_append.h", "mxattn.h", "mxattn_decode.h", "k_cache.hip",
+    "mxcache.h", "mxcache.hip", "mxcache_append.h", "mxattn.h", "mxattn_join.h", "mxattn_decode.h", "k_cache.hip",
     "k_attn_decode.hip", "mxattn_prompt.h", "k_attn_prompt.hip")]
 
 

@@ -1,5 +1,6 @@
 // k_attn_decode.hip -- attention over the 8-bit cache for few query rows.
 #include "mxattn_decode.h"
+#include "mxattn_join.h"
 
 namespace mxg {
 namespace {
@@ -7,17 +8,15 @@ namespace {
 template <int D>
 hipError_t go(const cache::AttnArgs &a, hipStream_t s)
 {
-    static_assert(attn::ROWS == kDecodeRows && attn::MAX_SPLITS == kMaxSplits, "host and kernel agree");
+    static_assert(attn::ROWS == kDecodeRows, "host and kernel agree");
     const int64_t tiles = (int64_t)a.c.seqs * a.c.kv_heads * a.row_tiles;
     const dim3 grid((unsigned)(tiles * a.splits)), block(attn::THREADS);
     if (a.c.shift < 6)
         hipLaunchKernelGGL((attn::decode_kernel<D, true>), grid, block, 0, s, a);
     else
         hipLaunchKernelGGL((attn::decode_kernel<D, false>), grid, block, 0, s, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.splits == 1) return e;
-    hipLaunchKernelGGL((attn::join_kernel<D>), dim3((unsigned)(tiles * attn::ROWS)), dim3(attn::JOIN_THREADS), 0, s, a);
-    return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || a.splits == 1 ? e : attn::launch_join<D, attn::ROWS>(a, tiles, s);
 }
 
 } // namespace

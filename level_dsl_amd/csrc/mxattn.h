@@ -46,33 +46,35 @@ __device__ __forceinline__ Range range_of(const AttnArgs &p, int ctx, int pmin, 
 __device__ __forceinline__ int position(const Seq &q, int64_t i) { return (int)max((int64_t)q.first + i, (int64_t)-1); }
 
 // The pages of a block's four chunks (page sizes are multiples of 16; SMALL:
-// below 64, otherwise all four lie in one), -1 where there is none.
-// Wave-uniform, through the scalar cache.
+// below 64, otherwise all four lie in one), -1 where the table gives none.
+// Wave-uniform, through the scalar cache; an entry is looked at only where it
+// is used, so that a load can be in flight until then.  A chunk past the
+// visible keys repeats the last one's (its tokens are masked by position).
 template <bool SMALL>
 struct Ids {
-    int id[SMALL ? 4 : 1];
+    int entry[SMALL ? 4 : 1], pages;
+    __device__ __forceinline__ int id(int j) const { return (unsigned)entry[j] < (unsigned)pages ? entry[j] : -1; }
     __device__ __forceinline__ int of(int chunk) const
     {
-        if constexpr (!SMALL) return id[0];
-        else return chunk == 0 ? id[0] : chunk == 1 ? id[1] : chunk == 2 ? id[2] : id[3];
+        if constexpr (!SMALL) return id(0);
+        else return chunk == 0 ? id(0) : chunk == 1 ? id(1) : chunk == 2 ? id(2) : id(3);
     }
     __device__ __forceinline__ bool all() const
     {
-        if constexpr (!SMALL) return id[0] >= 0;
-        else return (id[0] | id[1] | id[2] | id[3]) >= 0;
+        if constexpr (!SMALL) return id(0) >= 0;
+        else return (id(0) | id(1) | id(2) | id(3)) >= 0;
     }
 };
-// row: the sequence's row of the page table; t0 < hi
+// row: the sequence's row of the page table; t0 < hi, and hi is inside the table's reach
 template <bool SMALL>
 __device__ __forceinline__ Ids<SMALL> ids_of(const Pages &c, const int32_t *row, int t0, int hi)
 {
     Ids<SMALL> r;
+    r.pages = c.pages;
 #pragma unroll
     for (int j = 0; j < (SMALL ? 4 : 1); ++j) {
-        const int t = t0 + 16 * j;
-        const int at = min(t, hi - 1) >> c.shift;   // hi is inside the table's reach
-        const int id = *(const __attribute__((address_space(4))) int32_t *)(uintptr_t)(row + at);
-        r.id[j] = t < hi && (unsigned)id < (unsigned)c.pages ? id : -1;
+        const int at = min(t0 + 16 * j, hi - 1) >> c.shift;
+        r.entry[j] = *(const __attribute__((address_space(4))) int32_t *)(uintptr_t)(row + at);
     }
     return r;
 }

@@ -306,70 +306,5 @@ __global__ __launch_bounds__(THREADS, 2) void decode_kernel(AttnArgs p)
     }
 }
 
-// The splits' partial sums of one row, joined in a fixed order: lane group q
-// of 256 / (D / 4) adds splits q, q + groups, ..., then the groups are added in
-// turn.  The weights 2^(m_k - m) of all splits are computed once, by one wave.
-constexpr int JOIN_THREADS = 256, MAX_SPLITS = 64;
-template <int D>
-__global__ __launch_bounds__(JOIN_THREADS) void join_kernel(AttnArgs p)
-{
-    constexpr int LANES = D / 4, GROUPS = JOIN_THREADS / LANES;
-    constexpr int64_t PITCH = ROWS * (D + 2);
-    const Pages &c = p.c;
-    const int r = blockIdx.x % ROWS;
-    const int64_t tile = blockIdx.x / ROWS;
-    int64_t bid = tile;
-    const int rt = (int)(bid % p.row_tiles);
-    bid /= p.row_tiles;
-    const int head = (int)(bid % c.kv_heads), s = (int)(bid / c.kv_heads);
-    const Seq q = cache::sequence(c, s);
-    const int G = p.group;
-    const int64_t row = (int64_t)rt * ROWS + r;
-    if (row >= (int64_t)q.n * G) return;
-    const float *const part = p.ws + tile * p.splits * PITCH;
-
-    __shared__ float weight[MAX_SPLITS], total[2];
-    __shared__ v4f sums[GROUPS][LANES];
-    const int tid = threadIdx.x;
-    if (tid < 64) {
-        float m = kNone, l = 0.0f;
-        if (tid < p.splits) {
-            m = part[tid * PITCH + ROWS * D + r];
-            l = part[tid * PITCH + ROWS * D + ROWS + r];
-        }
-        float mt = m;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) mt = fmaxf(mt, __shfl_xor(mt, d, 64));
-        const float mu = mt == kNone ? 0.0f : mt;
-        const float w = __builtin_amdgcn_exp2f(m - mu);
-        l *= w;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d, 64);
-        weight[tid] = w;
-        if (tid == 0) {
-            total[0] = mu;
-            total[1] = l;
-        }
-    }
-    __syncthreads();
-    const int d4 = tid % LANES, g = tid / LANES;
-    v4f v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int k = g; k < p.splits; k += GROUPS)
-        v += *reinterpret_cast<const v4f *>(part + k * PITCH + r * D + 4 * d4) * weight[k];
-    sums[g][d4] = v;
-    __syncthreads();
-    if (g) return;
-#pragma unroll
-    for (int k = 1; k < GROUPS; ++k) v += sums[k][d4];
-    const float l = total[1];
-    v *= l == 0.0f ? 0.0f : 1.0f / l;
-    const int64_t token = q.q0 + row / G;
-    const int h = head * G + (int)(row % G);
-    *reinterpret_cast<v2i *>(p.O + token * p.o_stride + (int64_t)h * D + 4 * d4) =
-        v2i{(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3])};
-    if (tid == 0 && p.lse) p.lse[token * p.q_heads + h] = (total[0] + __builtin_log2f(l)) * kLn2;
-}
-
 } // namespace attn
 } // namespace mxg

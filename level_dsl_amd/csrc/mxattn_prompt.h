@@ -18,7 +18,8 @@
 // Blocks beyond a wave's own rows (causality, the window) are skipped by the
 // wave; whole blocks take a path without masks.  The running maximum lags as
 // in the decode kernel (rescaling 64 registers at every block otherwise).
-// The longest rows' workgroups start first.
+// The longest rows' workgroups start first.  Few rows over many keys are split
+// along the keys.
 #pragma once
 
 #include "mxattn.h"
@@ -32,7 +33,8 @@ using namespace attn;
 
 constexpr int WAVES = 4, THREADS = 64 * WAVES, WAVE_ROWS = 32, ROWS = WAVES * WAVE_ROWS;
 
-template <int D, bool SMALL>
+// SPLIT: an instantiation of its own, whose epilogue costs the other no registers
+template <int D, bool SMALL, bool SPLIT>
 __global__ __launch_bounds__(THREADS, 2) void kernel(AttnArgs p)
 {
     constexpr int CH = D / 32;      // 16-byte key chunks per lane and token
@@ -43,6 +45,8 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(AttnArgs p)
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r32 = lane & 31, h = lane >> 5;
     int64_t bid = blockIdx.x;
+    const int sp = SPLIT ? (int)(bid % p.splits) : 0;
+    if constexpr (SPLIT) bid /= p.splits;
     const int head = (int)(bid % c.kv_heads);
     bid /= c.kv_heads;
     const int s = (int)(bid % c.seqs);
@@ -72,9 +76,12 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(AttnArgs p)
         T::template load_values<WAVES>(c, ids, head_at, page, t0, wave, dst + T::K_BYTES);
     };
     Ids<SMALL> here = {}, next = {};
-    if (rg.count > 0) {
-        here = ids_of<SMALL>(c, table, rg.start(0), rg.hi);
-        fetch(buf0, here, rg.start(0));
+    // this split's blocks
+    const int per = SPLIT ? (rg.count + p.splits - 1) / p.splits : rg.count;
+    const int b0 = sp * per, b1 = min(rg.count, b0 + per);
+    if (b0 < b1) {
+        here = ids_of<SMALL>(c, table, rg.start(b0), rg.hi);
+        fetch(buf0, here, rg.start(b0));
     }
 
     v8bf qf[2 * CH];
@@ -197,7 +204,7 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(AttnArgs p)
         // the block has landed for every wave, and the other buffer is read out
         wait_vmem();
         __syncthreads();
-        if (i + 1 < rg.count) {
+        if (i + 1 < b1) {
             next = ids_of<SMALL>(c, table, rg.start(i + 1), rg.hi);
             fetch(other, next, rg.start(i + 1));
         }
@@ -214,13 +221,30 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(AttnArgs p)
         }
         here = next;
     };
-    for (int i = 0; i < rg.count; i += 2) {
+    for (int i = b0; i < b1; i += 2) {
         step(i, buf0, buf1);
-        if (i + 1 < rg.count) step(i + 1, buf1, buf0);
+        if (i + 1 < b1) step(i + 1, buf1, buf0);
     }
 
     l += __shfl_xor(l, 32, 64);
     if (!live) return;
+    if constexpr (SPLIT) {
+        // a part of its own for every split of the tile, joined by a second kernel
+        const int64_t tile = (((int64_t)s * c.kv_heads + head) * p.row_tiles + rt) * p.splits + sp;
+        float *const part = p.ws + tile * (ROWS * (D + 2));
+        const int r = wave * WAVE_ROWS + r32;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<v4f *>(part + r * D + 32 * d + 8 * e + 4 * h) =
+                    v4f{o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2], o[d][4 * e + 3]};
+        if (h == 0) {
+            part[ROWS * D + r] = m;
+            part[ROWS * D + ROWS + r] = l;
+        }
+        return;
+    }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     // column r32, rows (dims) 32 d + 8 e + 4 h .. + 3
     uint16_t *const dst = p.O + (q.q0 + qi) * p.o_stride + (int64_t)(head * G + qh) * D;

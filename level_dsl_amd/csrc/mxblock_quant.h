@@ -22,14 +22,34 @@ namespace block_quant {
 
 constexpr int THREADS = 256;
 
-// a = max(largest magnitude, 2^-100), as bits; scale a / MAX, codes x * (MAX / a)
+// a = max(largest magnitude, 2^-100), as bits; scale a / MAX, codes x * (MAX /
+// a).  a / MAX as a product with the rounded reciprocal and one correction by
+// the exact remainder: correctly rounded like the division (Markstein), in
+// three instructions (a NaN or an infinity gives NaN).
 template <int FMT>
 __device__ __forceinline__ float inverse(uint32_t m, float &scale)
 {
-    constexpr float MAX = FMT == 0 ? 448.0f : 57344.0f;
+    constexpr float MAX = FMT == 0 ? 448.0f : 57344.0f, ONE = 1.0f / MAX;
     const float a = __builtin_bit_cast(float, max(m, (uint32_t)(127 - 100) << 23));
-    scale = a / MAX;
+    const float q = a * ONE;
+    scale = __builtin_fmaf(__builtin_fmaf(-q, MAX, a), ONE, q);
     return MAX / a;
+}
+
+// Maximum over the 16 lanes of a row (row rotations in the ALU, no LDS).
+template <int N>
+__device__ __forceinline__ uint32_t max_ror(uint32_t x)
+{
+    return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x120 + N, 0xf, 0xf, false));
+}
+__device__ __forceinline__ uint32_t max16(uint32_t x) { return max_ror<1>(max_ror<2>(max_ror<4>(max_ror<8>(x)))); }
+// and with the neighbouring 16 lanes
+__device__ __forceinline__ uint32_t max32(uint32_t x)
+{
+    x = max16(x);
+    const auto u = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    const uint32_t u0 = u[0], u1 = u[1];
+    return max(u0, u1);
 }
 
 template <int FMT, bool XBF16, bool TILE>
@@ -55,31 +75,27 @@ __global__ __launch_bounds__(THREADS) void kernel(block::QuantArgs p)
     const int lc = lane % LPR;                                     // column group
     const int lr = wave * 32 + (lane / LPR) * RPT;                 // first row
     const bool kin = k0 + CPL * lc < K;                            // K % 16 == 0: all columns or none
-    float f[RPT][CPL];
     uint32_t cm[CPL];
 #pragma unroll
     for (int c = 0; c < CPL; ++c) cm[c] = 0;
     uint32_t rm[RPT];
-    {
-        v4i x[RPT];
+    v4i x[RPT];             // as loaded: bf16 takes half the registers
+    auto bits = [&](int j, int c) MXG_INLINE -> uint32_t {
+        if constexpr (XBF16) return c & 1 ? (uint32_t)x[j][c / 2] & 0xffff0000u : (uint32_t)x[j][c / 2] << 16;
+        else return (uint32_t)x[j][c];
+    };
+    auto f = [&](int j, int c) MXG_INLINE { return __builtin_bit_cast(float, bits(j, c)); };
 #pragma unroll
-        for (int j = 0; j < RPT; ++j)
-            x[j] = load16_nt(rX, kin ? ((uint32_t)(lr + j) * K + k0 + CPL * lc) * ESZ : kOob);
+    for (int j = 0; j < RPT; ++j)
+        x[j] = load16_nt(rX, kin ? ((uint32_t)(lr + j) * K + k0 + CPL * lc) * ESZ : kOob);
 #pragma unroll
-        for (int j = 0; j < RPT; ++j) {
-            rm[j] = 0;
+    for (int j = 0; j < RPT; ++j) {
+        rm[j] = 0;
 #pragma unroll
-            for (int c = 0; c < CPL; ++c) {
-                uint32_t b;
-                if constexpr (XBF16)
-                    b = ((uint32_t)x[j][c / 2] >> (16 * (c & 1))) << 16;
-                else
-                    b = (uint32_t)x[j][c];
-                f[j][c] = __builtin_bit_cast(float, b);
-                b &= 0x7fffffffu;
-                cm[c] = max(cm[c], b);
-                rm[j] = max(rm[j], b);
-            }
+        for (int c = 0; c < CPL; ++c) {
+            const uint32_t b = bits(j, c) & 0x7fffffffu;
+            cm[c] = max(cm[c], b);
+            rm[j] = max(rm[j], b);
         }
     }
 
@@ -117,9 +133,7 @@ __global__ __launch_bounds__(THREADS) void kernel(block::QuantArgs p)
         for (int j = 0; j < RPT; ++j) {
             float inv = i_tile;
             if constexpr (!TILE) {
-                uint32_t m = rm[j];
-#pragma unroll
-                for (int d = 1; d < LPR; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
+                const uint32_t m = LPR == 16 ? max16(rm[j]) : max32(rm[j]);
                 float s;
                 inv = inverse<FMT>(m, s);
                 if (lc == 0 && lr + j < rows) p.scales[(r0 + lr + j) * p.KB + tk] = s;
@@ -127,8 +141,8 @@ __global__ __launch_bounds__(THREADS) void kernel(block::QuantArgs p)
             uint32_t w[CPL / 4];
 #pragma unroll
             for (int q = 0; q < CPL / 4; ++q) {
-                w[q] = quant::cvt_pair<FMT>(f[j][4 * q] * inv, f[j][4 * q + 1] * inv, 0u, false);
-                w[q] = quant::cvt_pair<FMT>(f[j][4 * q + 2] * inv, f[j][4 * q + 3] * inv, w[q], true);
+                w[q] = quant::cvt_pair<FMT>(f(j, 4 * q) * inv, f(j, 4 * q + 1) * inv, 0u, false);
+                w[q] = quant::cvt_pair<FMT>(f(j, 4 * q + 2) * inv, f(j, 4 * q + 3) * inv, w[q], true);
             }
             const uint32_t off = kin ? (uint32_t)(lr + j) * K + k0 + CPL * lc : kOob;
             if constexpr (XBF16)
@@ -149,8 +163,8 @@ __global__ __launch_bounds__(THREADS) void kernel(block::QuantArgs p)
             uint32_t w[RPT / 4];
 #pragma unroll
             for (int q = 0; q < RPT / 4; ++q) {
-                w[q] = quant::cvt_pair<FMT>(f[4 * q][c] * inv, f[4 * q + 1][c] * inv, 0u, false);
-                w[q] = quant::cvt_pair<FMT>(f[4 * q + 2][c] * inv, f[4 * q + 3][c] * inv, w[q], true);
+                w[q] = quant::cvt_pair<FMT>(f(4 * q, c) * inv, f(4 * q + 1, c) * inv, 0u, false);
+                w[q] = quant::cvt_pair<FMT>(f(4 * q + 2, c) * inv, f(4 * q + 3, c) * inv, w[q], true);
             }
             uint8_t *dst = turned + (CPL * lc + c) * PITCH + lr;
             if constexpr (XBF16)

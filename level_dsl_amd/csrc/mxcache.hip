@@ -84,26 +84,37 @@ int64_t append_steps(const mxgemm_cache *c, const mxgemm_batch *b)
     return std::min((q + c->page_size - 2) / c->page_size + 1, b->max_pages);
 }
 
-int64_t row_tiles(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads)
+int64_t rows_of(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads)
 {
-    const int64_t rows = std::min(b->max_q, b->rows) * (q_heads / c->kv_heads);
-    return (rows + mxg::kDecodeRows - 1) / mxg::kDecodeRows;
+    return std::min(b->max_q, b->rows) * (q_heads / c->kv_heads);
 }
 
 // The prompt kernel, or the decode kernel, which reads the keys once for every
-// 16 rows.
+// 16 rows: 8192 keys, 16 sequences, 8 kv heads, dim 128, 32 rows: decode kernel 77
+// us, prompt kernel 98; 48 rows: 109, 114; 72 rows, 1 sequence of 16384: 40, 30.
 bool use_prompt(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads)
 {
-    return std::min(b->max_q, b->rows) * (q_heads / c->kv_heads) > 32;
+    return rows_of(c, b, q_heads) > 48;
+}
+
+int tile_rows(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads)
+{
+    return use_prompt(c, b, q_heads) ? mxg::kPromptRows : mxg::kDecodeRows;
+}
+
+int64_t row_tiles(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads)
+{
+    const int r = tile_rows(c, b, q_heads);
+    return (rows_of(c, b, q_heads) + r - 1) / r;
 }
 
 // Splits of the visible keys: enough workgroups for two on each of the 256
-// CUs, but at least four 64-key blocks (one per wave) a split.  More of them cost
-// more than their balance gains (64 sequences of 4097 to 8192 tokens, 8 kv
-// heads: 1 split 160 us, 2: 176, 4: 173).
+// CUs, but at least four 64-key blocks a split (one per wave of the decode
+// kernel).  More of them cost more than their balance gains (decode, 64
+// sequences of 4097 to 8192 tokens, 8 kv heads: 1 split 160 us, 2: 176, 4:
+// 173).
 int choose_splits(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads, int64_t window)
 {
-    if (use_prompt(c, b, q_heads)) return 1;
     const int64_t tiles = b->seqs * c->kv_heads * row_tiles(c, b, q_heads);
     const int64_t reach = std::min(b->max_ctx, b->max_pages * c->page_size);
     const int64_t keys = window ? std::min(reach, window + std::min(b->max_q, b->rows)) : reach;
@@ -116,7 +127,7 @@ int choose_splits(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads, int
 int64_t workspace(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads, int splits)
 {
     if (splits == 1) return 0;
-    return b->seqs * c->kv_heads * row_tiles(c, b, q_heads) * splits * mxg::kDecodeRows * (c->head_dim + 2) * 4;
+    return b->seqs * c->kv_heads * row_tiles(c, b, q_heads) * splits * tile_rows(c, b, q_heads) * (c->head_dim + 2) * 4;
 }
 
 bool heads_ok(const mxgemm_cache *c, int q_heads)
@@ -128,6 +139,7 @@ bool grid_ok(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads)
 {
     // 2^31 tokens times 4096 heads fit 64 bits; the product of three counts may not
     const int64_t t = row_tiles(c, b, q_heads);
+    // (splits are taken only while they keep the grid small)
     return t <= kMaxGrid && b->seqs * c->kv_heads <= kMaxGrid / t;
 }
 

@@ -179,6 +179,14 @@ def test_attend_long_context_splits(gemm):
     run_case(gemm, 1, 4, 64, 16, [3, 1], [4097, 2], window=1000, sinks=5)
 
 
+@pytest.mark.parametrize("window,sinks", [(0, 0), (700, 3)])
+def test_attend_few_rows_over_many_keys(gemm, window, sinks):
+    """More rows than the decode kernel takes, few enough that the keys are split."""
+    run_case(gemm, 1, 8, 128, 64, [20], [3000], window, sinks)
+    run_case(gemm, 2, 7, 64, 16, [9, 30], [1500, 40], window, sinks)
+    run_case(gemm, 1, 4, 128, 32, [33, 1], [1025, 2000], window, sinks, max_ctx=5000)
+
+
 def test_attend_rows_that_see_nothing(gemm):
     """More new tokens than the context holds: the first rows lie before
     position zero and get zeros; an empty context; pages that are hidden."""
