@@ -286,6 +286,31 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(block::Args p)
     // ---- epilogue -------------------------------------------------------------
     const int esz = p.out_bf16 ? 2 : 4;
     const rsrc_t rC = make_rsrc((uint8_t *)p.C + (size_t)m0 * p.N * esz, (uint32_t)rows_a * p.N * esz);
+    if (p.out_bf16 && p.c_vec == 2) {
+        // rows of 8 bf16: column tiles j and j + 1 trade the odd lane groups of
+        // one for the even groups of the other, so that a lane holds eight
+        // consecutive columns of tile j (g even) or j + 1 (g odd)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int m = wm * 64 + 16 * i + r16;
+#pragma unroll
+            for (int j = 0; j < NT; j += 2) {
+                v4f lo, hi;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x = acc[i][j][e], y = acc[i][j + 1][e];
+                    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x),
+                                                                    __builtin_bit_cast(uint32_t, y), false, false);
+                    const uint32_t r0 = r[0], r1 = r[1];
+                    lo[e] = __builtin_bit_cast(float, r0);
+                    hi[e] = __builtin_bit_cast(float, r1);
+                }
+                const int n = n0 + wn * 16 * NT + 16 * (j + (g & 1)) + 8 * (g >> 1);
+                store_bf16x8(rC, (uint32_t)m * p.N + n, n, p.N, lo, hi, p.use_acc);
+            }
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
         const int m = wm * 64 + 16 * i + r16;
