@@ -450,8 +450,8 @@ int mxgemm_run_block128(mxgemm_t h, const void *A, const float *A_scale, int fmt
  * A block holding a NaN or an infinity becomes NaN whole.
  *
  * Checks (pure host): rows, fmt, x_dtype, 1 <= R <= MXGEMM_MAX_M, 16 <= K <=
- * MXGEMM_MAX_K, K % 16 == 0, R * K <= MXGEMM_MAX_QELEMS (with codes_t also
- * R <= MXGEMM_MAX_K), X and codes 16-byte aligned, scales 4-byte aligned, all
+ * MXGEMM_MAX_K, K % 16 == 0, R * K <= MXGEMM_MAX_QELEMS in fewer than 2^24
+ * tiles of 128 x 128 (with codes_t also R <= MXGEMM_MAX_K), X and codes 16-byte aligned, scales 4-byte aligned, all
  * buffers disjoint. */
 int mxgemm_validate_quantize_block128(const void *X, int x_dtype, int64_t R, int64_t K, int rows,
                                       int fmt, const uint8_t *codes, const float *scales,
@@ -516,8 +516,8 @@ typedef struct mxgemm_batch {
  * Checks (pure host): pointers, x_dtype, page_size, head_dim, 1 <= kv_heads
  * <= 1024, 1 <= pages < 2^31, 1 <= seqs, rows, max_q, max_pages, max_ctx <
  * 2^31, kv_stride >= kv_heads * head_dim and a multiple of 8, K, V and codes
- * 16-byte aligned, int32 arrays 4-byte aligned; seqs * pages reached * kv_heads
- * < 2^30.  No buffer that is written may overlap another. */
+ * 16-byte aligned, int32 arrays 4-byte aligned; seqs * (pages that max_q tokens
+ * reach) < 2^24.  No buffer that is written may overlap another. */
 int mxgemm_validate_cache_append(const mxgemm_cache *cache, const mxgemm_batch *batch,
                                  const void *K, const void *V, int x_dtype, int64_t kv_stride);
 int mxgemm_cache_append(mxgemm_t h, const mxgemm_cache *cache, const mxgemm_batch *batch,
@@ -546,7 +546,8 @@ int mxgemm_cache_append(mxgemm_t h, const mxgemm_cache *cache, const mxgemm_batc
  * Keeps nothing between calls; captured calls follow the device arrays.
  *
  * Checks (pure host): those of the append where they apply; q_heads a
- * multiple of kv_heads, at most 4096; q_stride, o_stride >= q_heads *
+ * multiple of kv_heads, at most 4096; seqs * kv_heads * ceil(max_q * q_heads /
+ * kv_heads / 16) < 2^24; q_stride, o_stride >= q_heads *
  * head_dim, multiples of 8; Q, O 16-byte aligned; window, sinks >= 0, sinks
  * only with a window; softmax_scale finite; ws aligned and large enough if given
  * (MXGEMM_ERR_WORKSPACE). */

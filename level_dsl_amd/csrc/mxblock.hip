@@ -101,7 +101,7 @@ int mxgemm_validate_quantize_block128(const void *X, int x_dtype, int64_t R, int
     if (x_dtype != MXGEMM_X_F32 && x_dtype != MXGEMM_X_BF16) return MXGEMM_ERR_DTYPE;
     if (rows != 1 && rows != 128) return MXGEMM_ERR_SHAPE;
     if (R < 1 || K < 16 || R > MXGEMM_MAX_M || K > MXGEMM_MAX_K || K % 16 != 0 || R * K > MXGEMM_MAX_QELEMS ||
-        (codes_t && R > MXGEMM_MAX_K))
+        (codes_t && R > MXGEMM_MAX_K) || (R + 127) / 128 * ((K + 127) / 128) >= (int64_t)1 << 24)
         return MXGEMM_ERR_SHAPE;
     if (((uintptr_t)X | (uintptr_t)codes | (uintptr_t)codes_t) & 15u) return MXGEMM_ERR_ALIGN;
     if (((uintptr_t)scales | (uintptr_t)scales_t) & 3u) return MXGEMM_ERR_ALIGN;

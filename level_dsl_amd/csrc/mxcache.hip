@@ -15,7 +15,7 @@ using mxg::overlaps;
 namespace {
 
 constexpr int64_t kMaxInt = ((int64_t)1 << 31) - 1;
-constexpr int64_t kMaxGrid = (int64_t)1 << 30;
+constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;  // workgroups of 256 threads: 2^32 work-items are too many
 
 int page_shift(int page_size)
 {
@@ -117,7 +117,7 @@ int choose_splits(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads, int
 {
     const int64_t tiles = b->seqs * c->kv_heads * row_tiles(c, b, q_heads);
     const int64_t reach = std::min(b->max_ctx, b->max_pages * c->page_size);
-    const int64_t keys = window ? std::min(reach, window + std::min(b->max_q, b->rows)) : reach;
+    const int64_t keys = window && window < reach ? std::min(reach, window + std::min(b->max_q, b->rows)) : reach;
     const int64_t blocks = (keys + 63) / 64;
     int64_t s = (512 + tiles - 1) / tiles;
     s = std::min({s, blocks / 4, (int64_t)mxg::kMaxSplits});
@@ -135,11 +135,10 @@ bool heads_ok(const mxgemm_cache *c, int q_heads)
     return q_heads >= 1 && q_heads <= 4096 && q_heads % c->kv_heads == 0;
 }
 
+// (splits are taken only while they keep the grid small)
 bool grid_ok(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads)
 {
-    // 2^31 tokens times 4096 heads fit 64 bits; the product of three counts may not
     const int64_t t = row_tiles(c, b, q_heads);
-    // (splits are taken only while they keep the grid small)
     return t <= kMaxGrid && b->seqs * c->kv_heads <= kMaxGrid / t;
 }
 
@@ -156,7 +155,7 @@ int mxgemm_validate_cache_append(const mxgemm_cache *cache, const mxgemm_batch *
     if (x_dtype != MXGEMM_X_F32 && x_dtype != MXGEMM_X_BF16) return MXGEMM_ERR_DTYPE;
     const int64_t width = (int64_t)cache->kv_heads * cache->head_dim;
     if (kv_stride < width || kv_stride > kMaxInt || kv_stride % 8 != 0) return MXGEMM_ERR_SHAPE;
-    if (batch->seqs > kMaxGrid / (append_steps(cache, batch) * cache->kv_heads)) return MXGEMM_ERR_SHAPE;
+    if (batch->seqs > kMaxGrid / append_steps(cache, batch)) return MXGEMM_ERR_SHAPE;
     if (((uintptr_t)K | (uintptr_t)V) & 15u) return MXGEMM_ERR_ALIGN;
     const uint64_t x = ((uint64_t)(batch->rows - 1) * kv_stride + width) * (x_dtype == MXGEMM_X_F32 ? 4u : 2u);
     const uint64_t n = code_bytes(cache), ns = (uint64_t)cache->pages * cache->kv_heads;

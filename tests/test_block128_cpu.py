@@ -54,6 +54,11 @@ def vq(**kw):
     ({"K": 0}, SHAPE), ({"K": (1 << 21) + 16}, SHAPE), ({"R": (1 << 21) + 1}, SHAPE),
     ({"R": (1 << 21) + 1, "K": 16, "codes_t": 0, "scales_t": 0, "X": 1 << 40, "codes": 1 << 41,
       "scales": 1 << 42}, OK),
+    # 2^24 workgroups of 256 threads are one too many
+    ({"R": 1 << 30, "K": 144, "codes_t": 0, "scales_t": 0, "X": 1 << 44, "codes": 1 << 45,
+      "scales": 1 << 46}, SHAPE),
+    ({"R": (1 << 30) - 128, "K": 144, "codes_t": 0, "scales_t": 0, "X": 1 << 44, "codes": 1 << 45,
+      "scales": 1 << 46}, OK),
     ({"X": X + 4}, ALIGN), ({"codes": Q + 8}, ALIGN), ({"codes_t": QT + 4}, ALIGN), ({"scales": S + 2}, ALIGN),
     ({"scales_t": ST + 3}, ALIGN),
     ({"codes": X + 100 * 144 * 4 - 16}, ALIAS), ({"codes": X + 100 * 144 * 4}, OK), ({"scales": Q + 4}, ALIAS),

@@ -49,6 +49,8 @@ def va(kw):
     ({"kv_stride": 260}, SHAPE), ({"kv_stride": 264}, OK), ({"K": K + 8}, ALIGN), ({"V": V + 4}, ALIGN),
     # more workgroups than a grid holds
     ({"seqs": 1 << 30, "max_pages": 1, "page_table": 1 << 44, "q_start": 1 << 45, "ctx_len": 1 << 46}, SHAPE),
+    ({"seqs": (1 << 24) - 1, "max_pages": 1, "page_table": 1 << 44, "q_start": 1 << 45, "ctx_len": 1 << 46}, OK),
+    ({"seqs": 1 << 24, "max_pages": 1, "page_table": 1 << 44, "q_start": 1 << 45, "ctx_len": 1 << 46}, SHAPE),
     ({"v_codes": 16 * MB + 1638400}, OK), ({"v_codes": 16 * MB + 1638400 - 16}, ALIAS),
     ({"k_scales": 16 * MB}, ALIAS), ({"v_scales": 32 * MB + 4}, ALIAS), ({"K": 16 * MB}, ALIAS),
     ({"V": 48 * MB + 16}, ALIAS), ({"k_scales": 80 * MB + 4 * 20 * 4 - 1}, ALIAS), ({"k_scales": 81 * MB}, ALIAS),
@@ -72,6 +74,7 @@ def vt(kw):
     ({"Q": 0}, NULL), ({"O": 0}, NULL), ({"lse": 0}, OK), ({"q_heads": 7}, SHAPE), ({"q_heads": 0}, SHAPE),
     ({"q_heads": 6, "q_stride": 768, "o_stride": 768}, OK), ({"q_heads": 4098, "q_stride": 1 << 20}, SHAPE),
     ({"q_stride": 1016}, SHAPE), ({"o_stride": 1016}, SHAPE), ({"q_stride": 1028}, SHAPE), ({"q_stride": 2048}, OK),
+    ({"window": (1 << 63) - 1, "ws": WSP, "ws_bytes": 64 * MB}, OK),
     ({"window": -1}, SHAPE), ({"sinks": 4}, SHAPE), ({"sinks": 4, "window": 16}, OK),
     ({"sinks": -1, "window": 16}, SHAPE), ({"window": 1 << 40}, OK),
     ({"softmax_scale": float("nan")}, SHAPE), ({"softmax_scale": float("inf")}, SHAPE), ({"softmax_scale": 0.0}, OK),
