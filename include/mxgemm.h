@@ -401,8 +401,9 @@ int mxgemm_quantize(mxgemm_t h, const void *X, int x_dtype, int64_t R, int64_t K
  *   A        M x K codes, row-major; As  M x KB fp32, KB = ceil(K / 128);
  *   B        N x K codes, K contiguous; Bs  ceil(N / b_rows) x KB fp32;
  *   C        M x N fp32 or bf16, as for mxgemm_run.
- * K is a multiple of 16 (the last block may be short), scales may be any
- * fp32 numbers.
+ * K is a multiple of 16 (the last block may be short).  The product of two
+ * scales is taken first, in fp32: where it overflows, the outputs of that row
+ * and column are infinite or NaN.
  *
  * Arithmetic, by the handle's variant (mxgemm_set_variant):
  *   AUTO, LARGE, SKINNY   exact: the codes are widened to bf16 (exact), each
@@ -451,8 +452,8 @@ int mxgemm_run_block128(mxgemm_t h, const void *A, const float *A_scale, int fmt
  *
  * Checks (pure host): rows, fmt, x_dtype, 1 <= R <= MXGEMM_MAX_M, 16 <= K <=
  * MXGEMM_MAX_K, K % 16 == 0, R * K <= MXGEMM_MAX_QELEMS in fewer than 2^24
- * tiles of 128 x 128 (with codes_t also R <= MXGEMM_MAX_K), X and codes 16-byte aligned, scales 4-byte aligned, all
- * buffers disjoint. */
+ * tiles of 128 x 128 (with codes_t also R <= MXGEMM_MAX_K), X and codes
+ * 16-byte aligned, scales 4-byte aligned, all buffers disjoint. */
 int mxgemm_validate_quantize_block128(const void *X, int x_dtype, int64_t R, int64_t K, int rows,
                                       int fmt, const uint8_t *codes, const float *scales,
                                       const uint8_t *codes_t, const float *scales_t);
@@ -516,8 +517,8 @@ typedef struct mxgemm_batch {
  * Checks (pure host): pointers, x_dtype, page_size, head_dim, 1 <= kv_heads
  * <= 1024, 1 <= pages < 2^31, 1 <= seqs, rows, max_q, max_pages, max_ctx <
  * 2^31, kv_stride >= kv_heads * head_dim and a multiple of 8, K, V and codes
- * 16-byte aligned, int32 arrays 4-byte aligned; seqs * (pages that max_q tokens
- * reach) < 2^24.  No buffer that is written may overlap another. */
+ * 16-byte aligned, int32 arrays 4-byte aligned; seqs * (pages that max_q
+ * tokens reach) < 2^24.  No buffer that is written may overlap another. */
 int mxgemm_validate_cache_append(const mxgemm_cache *cache, const mxgemm_batch *batch,
                                  const void *K, const void *V, int x_dtype, int64_t kv_stride);
 int mxgemm_cache_append(mxgemm_t h, const mxgemm_cache *cache, const mxgemm_batch *batch,
@@ -536,9 +537,11 @@ int mxgemm_cache_append(mxgemm_t h, const mxgemm_cache *cache, const mxgemm_batc
  * logarithm of the softmax's sum.  Rows outside every sequence are left as
  * they were.
  *
- * Arithmetic: keys are widened exactly to bf16, scores, maximum, sum and
- * output are fp32; the probabilities are rounded to bf16 (2^-9 relative) as
- * the second product's operand, not in the sum.
+ * Arithmetic: keys and values are widened to bf16 with their scales, exactly
+ * for scale bytes 10 .. 246 (below, magnitudes under 2^-133 may be lost, above,
+ * those from 2^128 are infinite); scores, maximum, sum and output are fp32; the
+ * probabilities are rounded to bf16 (2^-8 relative at most) as the second
+ * product's operand, not in the sum.
  *
  * ws: mxgemm_cache_attention_workspace bytes, 256-byte aligned, lets few rows
  * over long contexts be split over the GPU; NULL / 0 never splits.  Calls
@@ -547,9 +550,9 @@ int mxgemm_cache_append(mxgemm_t h, const mxgemm_cache *cache, const mxgemm_batc
  *
  * Checks (pure host): those of the append where they apply; q_heads a
  * multiple of kv_heads, at most 4096; seqs * kv_heads * ceil(max_q * q_heads /
- * kv_heads / 16) < 2^24; q_stride, o_stride >= q_heads *
- * head_dim, multiples of 8; Q, O 16-byte aligned; window, sinks >= 0, sinks
- * only with a window; softmax_scale finite; ws aligned and large enough if given
+ * kv_heads / 16) < 2^24; q_stride, o_stride >= q_heads * head_dim, multiples
+ * of 8; Q, O 16-byte aligned; window, sinks >= 0, sinks only with a window;
+ * softmax_scale finite; ws aligned and large enough if given
  * (MXGEMM_ERR_WORKSPACE). */
 int64_t mxgemm_cache_attention_workspace(const mxgemm_cache *cache, const mxgemm_batch *batch,
                                          int q_heads, int64_t window);

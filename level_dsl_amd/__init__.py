@@ -618,7 +618,7 @@ class Batch:
 
     def struct(self, cache, rows: int) -> BatchStruct:
         """The mxgemm_batch of a call on `rows` tokens over `cache`."""
-        key = (rows, cache.page_size)
+        key = (rows, cache.page_size, self.max_q, self.max_ctx)
         got = self._structs.get(key)
         if got is None:
             t, q, c = self.tensors

@@ -2,7 +2,7 @@
 // (decode steps): the cache is streamed once, each block by one wave.
 //
 // A row is one (new token, query head of the group) pair of a sequence and kv
-// head, rows in token order; a workgroup of two waves takes 16 of them and a
+// head, rows in token order; a workgroup of four waves takes 16 of them and a
 // part of the visible keys (a split).  Keys come in blocks of 64, dealt to the
 // waves in turn.  Per block a wave computes
 //   S^T = K Q^T   16x16x32 bf16 MFMA, K's rows (tokens) by Q's columns (rows)

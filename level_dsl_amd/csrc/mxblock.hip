@@ -12,20 +12,24 @@ using mxg::overlaps;
 
 namespace {
 
-// The large tiles, or the small ones.  A grid of large tiles that fills its
-// last round of the 256 CUs to the share e runs at e times its full rate; the
-// small tiles need no such care and reach 0.77 PFLOP/s (1024 x 4096 x 4096:
-// 44 us, large 71 us), the large ones 0.93 exact (2048 x 4096 x 4096: 74 us)
-// and 1.9 native.
+// The large tiles, or the small ones.  Large tiles take as long for a partly
+// filled round of the 256 CUs as for a whole one, so they run at the share of
+// their full rate that the outputs are of the tiles of all rounds; the small
+// ones need no such care.  Measured (us, small / large exact / large native;
+// N = 4096 and K = 4096 unless given, the share in brackets):
+//   M = 1024  44 / 58 (50%) / 47 (25%)     M = 1280  61 / 57 (62%) / 48 (31%)
+//   M = 1536  64 / 58 (75%) / 48 (37%)     M = 2304  99 / 113 (56%) / 49 (56%)
+//   M = 2816  119 / 114 (69%) / 49 (69%)   M = 4352  181 / 171 (71%) / 103 (53%)
+//   N = 28672, K = 8192: M = 128  105 / 121 (44%) / 103 (22%)
+//                        M = 256  172 / 127 (87%) / 109 (44%)
 bool use_large(int variant, int64_t M, int64_t N)
 {
     if (variant == MXGEMM_VARIANT_SKINNY || M <= 64) return false;
     if (variant == MXGEMM_VARIANT_LARGE) return true;
     const bool native = variant == MXGEMM_VARIANT_LARGE_NATIVE;
     const int64_t bn = native ? 256 : 128;
-    const int64_t tiles = ((M + 255) / 256) * ((N + bn - 1) / bn);
-    const int64_t rounds = (tiles + 255) / 256;
-    return 100 * tiles >= (native ? 40 : 82) * 256 * rounds;
+    const int64_t rounds = ((M + 255) / 256 * ((N + bn - 1) / bn) + 255) / 256;
+    return M * N >= (native ? 28 : 60) * (256 * bn * 256 / 100) * rounds;
 }
 
 } // namespace

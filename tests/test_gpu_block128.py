@@ -57,9 +57,11 @@ def scaled(codes, f, s, rows):
     return x * s
 
 
-def check(gemm, M, N, K, fa=0, fb=0, rows_b=128, bf16=False, acc=False, seed=1, native=False, stream=None):
+def check(gemm, M, N, K, fa=0, fb=0, rows_b=128, bf16=False, acc=False, seed=1, native=False, stream=None,
+          where="cpu"):
+    """where: the device of the fp64 reference"""
     A, sa, B, sb = problem(M, N, K, fa, fb, rows_b, seed)
-    a, b = scaled(A, fa, sa, 1), scaled(B, fb, sb, rows_b)
+    a, b = scaled(A, fa, sa, 1).to(where), scaled(B, fb, sb, rows_b).to(where)
     ref, mag = a @ b.t(), a.abs() @ b.abs().t()
     dt = torch.bfloat16 if bf16 else torch.float32
     pad = 64
@@ -69,7 +71,7 @@ def check(gemm, M, N, K, fa=0, fb=0, rows_b=128, bf16=False, acc=False, seed=1, 
     if acc:
         C0 = torch.randn((M, N), generator=torch.Generator().manual_seed(seed + 1)).to(dt)
         C.copy_(C0)
-        ref, mag = ref + C0.double(), mag + C0.double().abs()
+        ref, mag = ref + C0.to(where).double(), mag + C0.to(where).double().abs()
     tol = (cdiv(K, 128) + 17) * 2.0 ** -24 * mag
     if native:
         p = torch.zeros_like(mag)
@@ -81,7 +83,7 @@ def check(gemm, M, N, K, fa=0, fb=0, rows_b=128, bf16=False, acc=False, seed=1, 
     to = [t.to(DEV) for t in (A, sa, B, sb)]
     gemm.block128(to[0], to[1], fa, to[2], to[3], fb, C, use_acc=acc, stream=stream)
     torch.cuda.synchronize()
-    got = C.double().cpu()
+    got = C.double().to(where)
     bad = ~((got - ref).abs() <= tol)
     assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} outside, worst {float(((got - ref).abs() / tol).max())}"
     assert (buf[:pad] == 7.0).all() and (buf[-pad:] == 7.0).all(), "store outside C"
@@ -110,6 +112,54 @@ def test_product_variants(gemm, variant, M, N, K, fa, fb, rows_b, bf16, acc):
         check(gemm, M, N, K, fa, fb, rows_b, bf16, acc, seed=M + K, native=variant == L.MXGEMM_VARIANT_LARGE_NATIVE)
     finally:
         gemm.set_variant(L.MXGEMM_VARIANT_AUTO)
+
+
+# the wider small tiles, taken where they still give a workgroup to every CU
+@pytest.mark.parametrize("M,N,K", [(20, 16391, 272), (32, 8200, 400), (33, 16390, 144), (64, 8198, 272),
+                                   (300, 4104, 1040), (1, 28680, 16)])
+@pytest.mark.parametrize("fa,rows_b,bf16,acc", [(0, 128, True, False), (1, 1, False, True)])
+def test_product_many_columns(gemm, M, N, K, fa, rows_b, bf16, acc):
+    check(gemm, M, N, K, fa, 0, rows_b, bf16, acc, seed=M, where=DEV)
+
+
+# the fp8 MFMA, taken where 256 x 256 tiles fill the GPU well enough
+@pytest.mark.parametrize("M,N,K", [(2600, 2080, 400), (2561, 2310, 144), (2817, 2050, 16), (257, 21000, 1168)])
+@pytest.mark.parametrize("fa,fb,rows_b,bf16,acc", [(0, 0, 128, True, False), (1, 0, 1, False, True),
+                                                  (0, 1, 128, False, False), (1, 1, 1, True, True)])
+def test_product_native(gemm, M, N, K, fa, fb, rows_b, bf16, acc):
+    gemm.set_variant(L.MXGEMM_VARIANT_LARGE_NATIVE)
+    try:
+        got = check(gemm, M, N, K, fa, fb, rows_b, bf16, acc, seed=M + K, native=True, where=DEV)
+    finally:
+        gemm.set_variant(L.MXGEMM_VARIANT_AUTO)
+    assert got.isfinite().all()
+
+
+def test_product_past_32_bits(gemm):
+    """Operand and output bytes past 2^32: the last rows and columns agree with
+    the same rows and columns multiplied alone."""
+    g = torch.Generator(DEV).manual_seed(3)
+    N, K = 140001, 32768
+    B = torch.randint(0, 120, (N, K), generator=g, dtype=torch.uint8, device=DEV)
+    sb = torch.rand((cdiv(N, 128), K // 128), generator=g, device=DEV)
+    A = torch.randint(0, 120, (5, K), generator=g, dtype=torch.uint8, device=DEV)
+    sa = torch.rand((5, K // 128), generator=g, device=DEV)
+    got = gemm.block128(A, sa, 0, B, sb, 0, torch.empty((5, N), device=DEV))
+    n0 = (N - 200) // 128 * 128
+    assert n0 * K > 2 ** 32
+    a = A.view(F8[0]).double() * sa.double().repeat_interleave(128, 1)
+    b = B[n0:].view(F8[0]).double() * sb[n0 // 128:].double().repeat_interleave(128, 1) \
+        .repeat_interleave(128, 0)[:N - n0]
+    ref = a @ b.t().contiguous()              # codes and scales are positive: the sum of magnitudes too
+    assert ((got[:, n0:].double() - ref).abs() <= (K // 128 + 16) * 2.0 ** -24 * ref).all()
+    del B, b
+    M, N, K = 66000, 33000, 16
+    A = torch.randint(0, 120, (M, K), generator=g, dtype=torch.uint8, device=DEV)
+    B = torch.randint(0, 120, (N, K), generator=g, dtype=torch.uint8, device=DEV)
+    sa, sb = torch.rand((M, 1), generator=g, device=DEV), torch.rand((N, 1), generator=g, device=DEV)
+    got = gemm.block128(A, sa, 0, B, sb, 0, torch.empty((M, N), dtype=torch.bfloat16, device=DEV))
+    ref = (A[-300:].view(F8[0]).double() * sa[-300:]) @ (B.view(F8[0]).double() * sb).t().contiguous()
+    assert ((got[-300:].double() - ref).abs() <= 2.0 ** -8 * ref * 1.01).all()
 
 
 def test_product_special_values(gemm):
@@ -221,6 +271,20 @@ def test_quantize(gemm, R, K, rows, fmt, bf16):
     turn = gemm.quantize_block128(x.to(DEV), fmt, rows=rows, normal=False, transposed=True)
     assert np.array_equal(only[0].cpu().numpy(), codes) and np.array_equal(only[1].cpu().numpy(), scales)
     assert np.array_equal(turn[0].cpu().numpy(), codes_t) and np.array_equal(turn[1].cpu().numpy(), scales_t)
+
+
+@pytest.mark.parametrize("rows", [1, 128])
+def test_quantize_past_32_bits(gemm, rows):
+    """More than 2^32 elements: the last rows' codes are those that the rows get
+    alone, and so are the transpose's."""
+    R, K = 2 ** 17 + 200, 2 ** 15 + 16
+    x = torch.randn((R, K), dtype=torch.bfloat16, device=DEV, generator=torch.Generator(DEV).manual_seed(1))
+    c, s, ct, st = gemm.quantize_block128(x, 1, rows=rows, transposed=True)
+    r0 = 2 ** 17
+    assert c[r0:].data_ptr() - c.data_ptr() > 2 ** 32
+    tail = gemm.quantize_block128(x[r0:], 1, rows=rows, transposed=True)
+    assert torch.equal(c[r0:], tail[0]) and torch.equal(s[r0 // rows:], tail[1])
+    assert torch.equal(ct[:, r0:], tail[2]) and torch.equal(st[:, r0 // 128:], tail[3])
 
 
 @pytest.mark.parametrize("rows", [1, 128])

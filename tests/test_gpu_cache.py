@@ -247,6 +247,46 @@ def test_attend_row_bound(gemm):
     compare(out[keep], ls[keep], *(x[keep] for x in (O, lse, to, tl)), 9)
 
 
+@pytest.mark.parametrize("n", [[1, 2], [70, 1]])
+def test_attend_shared_pages(gemm, n):
+    """Two sequences that read the same first pages, one of them twice."""
+    heads, dim, page = 2, 64, 16
+    table, q, cl, pages = ref.batch(2, n, [150, 100], page, 3)
+    c = ref.Cache(pages, heads, page, dim, 4)
+    fill(c, table, q, cl, 8)
+    table[1, :4] = table[0, :4]
+    table[1, 4] = table[0, 0]
+    Q = rand((sum(n), 8, dim), 1).bfloat16()
+    O, lse, to, tl = ref.attend(c, table, q, cl, Q, 0.125, 0, 0)
+    out, ls = upload(gemm, c).attend(L.Batch(table.to(DEV), q.to(DEV), cl.to(DEV), max_q=max(n)), Q.to(DEV))
+    compare(out, ls, O, lse, to, tl, sum(n))
+
+
+@pytest.mark.parametrize("n", [[1, 3], [60, 9]])
+@pytest.mark.parametrize("page,dim", [(64, 128), (16, 64)])
+def test_pages_past_32_bits(gemm, n, page, dim):
+    """Pages whose bytes lie past 2^32 of the codes: stored and read as the same
+    pages of a small cache."""
+    heads = 4
+    table, q, cl, pages = ref.batch(2, n, [150, 100], page, 3)
+    c = ref.Cache(pages, heads, page, dim, 4)
+    fill(c, table, q, cl - torch.tensor(n), 8)
+    K, V, Q = (rand((sum(n), h, dim), s).bfloat16().to(DEV) for h, s in ((heads, 1), (heads, 2), (8, 3)))
+    base = 2 ** 32 // (heads * page * dim) + 1
+    small, big = upload(gemm, c), L.KVCache.empty(gemm, base + pages, page, heads, dim)
+    for t, x in zip(big.tensors, small.tensors):
+        t[base:] = x
+    assert big.tensors[0][base:].data_ptr() - big.tensors[0].data_ptr() > 2 ** 32
+    got = []
+    for kv, at in ((small, 0), (big, base)):
+        b = L.Batch((table + at).to(DEV), q.to(DEV), cl.to(DEV), max_q=max(n))
+        kv.append(b, K, V)
+        got.append(kv.attend(b, Q))
+    assert all(torch.equal(t[base:], x) for t, x in zip(big.tensors, small.tensors))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert not big.tensors[0][:base].any() and not big.tensors[2][:base].any()
+
+
 def test_attend_strided_heads(gemm):
     """Q as a view of a fused projection, out as a view of a wider buffer."""
     kv, b, Q, out, ls = run_case(gemm, 2, 2, 64, 16, [3, 20], [30, 25], rows_after=0)
