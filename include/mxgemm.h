@@ -419,7 +419,8 @@ int mxgemm_quantize(mxgemm_t h, const void *X, int x_dtype, int64_t R, int64_t K
  *   SKINNY_NATIVE         MXGEMM_ERR_VARIANT: small shapes are bound by
  *       reading B and always run exact.
  * LARGE takes the 256-row tiles for M > 64 whatever the shape, SKINNY the
- * small tiles; AUTO and LARGE_NATIVE take the faster for the shape.
+ * small tiles (below 2^32 outputs); AUTO and LARGE_NATIVE take the faster for
+ * the shape.
  * Needs no workspace and no operand buffer, keeps nothing between calls, and
  * may be captured into a graph; calls on one handle may overlap.
  *

@@ -17,19 +17,21 @@ namespace {
 // their full rate that the outputs are of the tiles of all rounds; the small
 // ones need no such care.  Measured (us, small / large exact / large native;
 // N = 4096 and K = 4096 unless given, the share in brackets):
-//   M = 1024  44 / 58 (50%) / 47 (25%)     M = 1280  61 / 57 (62%) / 48 (31%)
-//   M = 1536  64 / 58 (75%) / 48 (37%)     M = 2304  99 / 113 (56%) / 49 (56%)
-//   M = 2816  119 / 114 (69%) / 49 (69%)   M = 4352  181 / 171 (71%) / 103 (53%)
-//   N = 28672, K = 8192: M = 128  105 / 121 (44%) / 103 (22%)
-//                        M = 256  172 / 127 (87%) / 109 (44%)
+//   M = 1024  41 / 58 (50%) / 47 (25%)     M = 1280  52 / 57 (62%) / 48 (31%)
+//   M = 1536  59 / 58 (75%) / 48 (37%)     M = 2304  87 / 113 (56%) / 49 (56%)
+//   M = 2816  108 / 114 (69%) / 52 (69%)   M = 4352  162 / 171 (71%) / 103 (53%)
+//   N = 28672, K = 8192: M = 128  94 / 121 (44%) / 103 (22%)
+//                        M = 256  149 / 131 (87%) / 114 (44%)
+// From 2^20 tiles of 64 x 64 on, the small ones' grid could pass 2^32 threads.
 bool use_large(int variant, int64_t M, int64_t N)
 {
-    if (variant == MXGEMM_VARIANT_SKINNY || M <= 64) return false;
-    if (variant == MXGEMM_VARIANT_LARGE) return true;
+    if (M <= 64) return false;
+    if (variant == MXGEMM_VARIANT_LARGE || (M + 63) / 64 * ((N + 63) / 64) >= (int64_t)1 << 20) return true;
+    if (variant == MXGEMM_VARIANT_SKINNY) return false;
     const bool native = variant == MXGEMM_VARIANT_LARGE_NATIVE;
     const int64_t bn = native ? 256 : 128;
     const int64_t rounds = ((M + 255) / 256 * ((N + bn - 1) / bn) + 255) / 256;
-    return M * N >= (native ? 28 : 60) * (256 * bn * 256 / 100) * rounds;
+    return M * N >= (native ? 28 : 73) * (256 * bn * 256 / 100) * rounds;
 }
 
 } // namespace

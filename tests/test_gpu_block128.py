@@ -135,6 +135,27 @@ def test_product_native(gemm, M, N, K, fa, fb, rows_b, bf16, acc):
     assert got.isfinite().all()
 
 
+@pytest.mark.parametrize("variant", [L.MXGEMM_VARIANT_AUTO, L.MXGEMM_VARIANT_SKINNY])
+@pytest.mark.parametrize("M", [2 ** 26 - 70, 2 ** 26 + 37])
+def test_product_many_rows(gemm, variant, M):
+    """As many rows as the small tiles take, and more."""
+    A, sa, B, sb = (t.to(DEV) for t in problem(4099, 24, 16, 0, 0, 1, 9))
+    n = cdiv(M, 4099)
+    gemm.set_variant(variant)
+    try:
+        got = gemm.block128(A.repeat(n, 1)[:M], sa.repeat(n, 1)[:M], 0, B, sb, 0,
+                            torch.empty((M, 24), dtype=torch.bfloat16, device=DEV))
+    finally:
+        gemm.set_variant(L.MXGEMM_VARIANT_AUTO)
+    a, b = scaled(A.cpu(), 0, sa.cpu(), 1), scaled(B.cpu(), 0, sb.cpu(), 1)
+    ref, mag = (a @ b.t()).to(DEV), (a.abs() @ b.abs().t()).to(DEV)
+    tol = 18 * 2.0 ** -24 * mag
+    tol += 2.0 ** -8 * (ref.abs() + tol)
+    for at in (0, M // 4099 // 2 * 4099, M // 4099 * 4099 - 4099, M - M % 4099):
+        x = got[at:at + 4099].double()
+        assert ((x - ref[:len(x)]).abs() <= tol[:len(x)]).all()
+
+
 def test_product_past_32_bits(gemm):
     """Operand and output bytes past 2^32: the last rows and columns agree with
     the same rows and columns multiplied alone."""
