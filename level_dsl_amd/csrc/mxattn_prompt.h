@@ -21,11 +21,13 @@
 // otherwise).  The longest rows' workgroups start first.  Few rows over many
 // keys are split along the keys.
 //
-// 2 x 2048 rows over 8192 keys, 32 / 8 heads, dim 128: 470 us, 930 TFLOP/s.
+// 2 x 2048 rows over 8192 keys, 32 / 8 heads, dim 128: 456 us, 960 TFLOP/s.
 // The SIMDs are busy issuing: per wave and block 32 MFMAs (1024 cycles) and
-// about 350 other vector instructions, a third of them the widening.  Widening
-// once for all four waves through LDS (540 us) and running the first product a
-// block ahead (540 us) spent as many instructions elsewhere.
+// about 280 other vector instructions (1300 cycles), 128 of them the widening.
+// Widening once for all four waves through LDS (540 us) and running the first
+// product a block ahead (540 us) spent as many instructions elsewhere.  Of a
+// SIMD's two waves the one in its products goes first (470 us without; at dim
+// 64, where the softmax is half the work, 305 us without and 323 us with).
 #pragma once
 
 #include "mxattn.h"
@@ -45,6 +47,7 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(AttnArgs p)
 {
     constexpr int CH = D / 32;      // 16-byte key chunks per lane and token
     constexpr int DT = D / 32;      // 32-row tiles of O^T
+    constexpr bool PRIO = D == 128; // the products before the other wave's softmax
     using T = Tile<D>;
     __shared__ __attribute__((aligned(1024))) uint8_t buf0[T::BYTES], buf1[T::BYTES];
     const Pages &c = p.c;
@@ -140,6 +143,7 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(AttnArgs p)
                 st[t] = mfma_bf16_32(hi, qf[2 * i + 1], st[t]);
             }
         }
+        if constexpr (PRIO) __builtin_amdgcn_s_setprio(0);
         float mx = kNone;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -190,6 +194,7 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(AttnArgs p)
                 pf[t][e >> 3][e & 7] = (__bf16)x;
             }
         }
+        if constexpr (PRIO) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const float vs = edge ? 1.0f : e8m0_to_f32(vb[t]);
