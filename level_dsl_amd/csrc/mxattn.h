@@ -168,24 +168,31 @@ __device__ __forceinline__ float max_groups(float x)
 // (normal bf16 numbers).
 __device__ __forceinline__ bool plain_scale(uint32_t b) { return b - (uint32_t)scale_lo<0>() <= (uint32_t)window_width<0>(); }
 
-// Bit e: whether some row of the tile sees token t + e, e = 0 .. 15.
-__device__ __forceinline__ uint32_t seen16(const Range &r, int id, int t)
+// The lowest n bits of 16 (none for n below zero).
+__device__ __forceinline__ uint32_t below16(int n) { return (1u << min(max(n, 0), 16)) - 1; }
+// Bit e: whether key t + e, e = 0 .. 15, lies in [lo, hi) or, below hi, in [0, sinks).
+__device__ __forceinline__ uint32_t seen16(int lo, int hi, int sinks, int t)
 {
-    uint32_t keep = 0;
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-        keep |= (id >= 0 && t + e < r.hi && (t + e >= r.lo || t + e < r.sinks) ? 1u : 0u) << e;
-    return keep;
+    return below16(hi - t) & (~below16(lo - t) | below16(sinks - t));
+}
+// all bits set where bit e of keep is
+__device__ __forceinline__ uint32_t spread(uint32_t keep, int e) { return (uint32_t)((int)(keep << (31 - e)) >> 31); }
+// x where m's bits are set, a masked score elsewhere, whatever x is
+__device__ __forceinline__ float score_or_none(uint32_t m, float x)
+{
+    return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x) & m) | (~m & 0xff800000u));
+}
+__device__ __forceinline__ float value_or_zero(uint32_t m, float x)
+{
+    return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & m);
 }
 // 16 codes with those of the cleared bits zeroed
 __device__ __forceinline__ v4i keep16(v4i x, uint32_t keep)
 {
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-        const uint32_t n = keep >> (4 * w);
-        const uint32_t m = ((n & 1u) ? 0xffu : 0u) | ((n & 2u) ? 0xff00u : 0u) | ((n & 4u) ? 0xff0000u : 0u) |
-                           ((n & 8u) ? 0xff000000u : 0u);
-        x[w] &= (int)m;
+        const uint32_t n = (keep >> (4 * w) & 15u) * 0x204081u & 0x01010101u;   // bit i to byte i
+        x[w] &= (int)((n << 8) - n);
     }
     return x;
 }

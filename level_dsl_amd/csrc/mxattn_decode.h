@@ -105,7 +105,7 @@ __global__ __launch_bounds__(THREADS, 2) void decode_kernel(AttnArgs p)
     const bool live = row < rows;
     const int qi = (int)((live ? row : row0) / G), qh = (int)((live ? row : row0) % G);
     const int pos = position(q, qi);
-    const int wlo = p.window ? pos - p.window : -0x7fffffff - 1;   // key > wlo is inside the window
+    const int from = p.window ? max(pos - p.window + 1, 0) : 0;    // the window's first key
     const float scale = fabsf(p.scale_log2);
     v8bf qf[2 * CH];
     {
@@ -186,6 +186,7 @@ __global__ __launch_bounds__(THREADS, 2) void decode_kernel(AttnArgs p)
         };
         v4f st[4];
         v8bf pf[2];
+        uint32_t see = 0xffff;      // which of the lane's keys its row sees
         // the values' byte came behind the keys: it is waited for with the values
         const bool whole = here.all() && t0 + BLOCK <= rg.hi && t0 + BLOCK - 1 <= pmin &&
                            (!p.window || t0 > pmax - p.window) &&
@@ -211,15 +212,13 @@ __global__ __launch_bounds__(THREADS, 2) void decode_kernel(AttnArgs p)
             next_keys();
             // chunk g's byte is held by the lanes with r16 / 4 = g
             const float ks = e8m0_to_f32((uint32_t)__shfl((int)kb_now, 4 * g, 64)) * scale;
-            const int id = here.of(g);
+            see = here.of(g) >= 0 ? seen16(from, min(pos + 1, rg.hi), p.sinks, t0 + 16 * g) : 0;
             float mx = kNone;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int key = t0 + 16 * g + 4 * t + e;
-                    const bool see = id >= 0 && key <= pos && key < rg.hi && (key > wlo || key < p.sinks);
-                    st[t][e] = see ? st[t][e] * ks : kNone;
+                    st[t][e] = score_or_none(spread(see, 4 * t + e), st[t][e] * ks);
                     mx = fmaxf(mx, st[t][e]);
                 }
             const float mu = follow(mx);
@@ -227,10 +226,8 @@ __global__ __launch_bounds__(THREADS, 2) void decode_kernel(AttnArgs p)
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    // masked: below every probability, so that it can be told apart
-                    const bool see = st[t][e] != kNone;
-                    st[t][e] = see ? __builtin_amdgcn_exp2f(st[t][e] - mu) : -1.0f;
-                    l += see ? st[t][e] : 0.0f;
+                    st[t][e] = __builtin_amdgcn_exp2f(st[t][e] - mu);   // 0 where masked
+                    l += st[t][e];
                 }
         }
         wait_values();
@@ -246,8 +243,8 @@ __global__ __launch_bounds__(THREADS, 2) void decode_kernel(AttnArgs p)
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    pf[t >> 1][4 * (t & 1) + e] = (__bf16)(st[t][e] == -1.0f ? 0.0f : st[t][e] * vs);
-            add(std::true_type{}, pf, 1.0f, seen16(rg, here.of(g), t0 + 16 * g));
+                    pf[t >> 1][4 * (t & 1) + e] = (__bf16)value_or_zero(spread(see, 4 * t + e), st[t][e] * vs);
+            add(std::true_type{}, pf, 1.0f, here.of(g) >= 0 ? seen16(rg.lo, rg.hi, rg.sinks, t0 + 16 * g) : 0);
         }
         wait_lds();           // the values' reads have returned
         if (more) {

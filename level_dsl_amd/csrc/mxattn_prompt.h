@@ -75,7 +75,7 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(AttnArgs p)
     const bool live = row < rows;
     const int qi = (int)((live ? row : row0) / G), qh = (int)((live ? row : row0) % G);
     const int pos = position(q, qi);
-    const int wlo = p.window ? pos - p.window : -0x7fffffff - 1;   // key > wlo is inside the window
+    const int from = p.window ? max(pos - p.window + 1, 0) : 0;    // the window's first key
     const float scale = fabsf(p.scale_log2);
 
     const uint32_t page1 = (uint32_t)D << c.shift, head_at = head * page1, page = page1 * c.kv_heads;
@@ -145,18 +145,15 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(AttnArgs p)
         }
         if constexpr (PRIO) __builtin_amdgcn_s_setprio(0);
         float mx = kNone;
+        uint32_t see[2] = {};       // which of the lane's keys its row sees
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const int key0 = t0 + 32 * t + 16 * h;
-            const int id = edge ? ids.of(2 * t + h) : 0;
             const float ks = edge ? e8m0_to_f32(kb[t]) * scale : 1.0f;
+            if constexpr (edge)
+                see[t] = ids.of(2 * t + h) >= 0 ? seen16(from, min(pos + 1, rg.hi), p.sinks, t0 + 32 * t + 16 * h) : 0;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                if constexpr (edge) {
-                    const int key = key0 + e;
-                    const bool see = id >= 0 && key <= pos && key < rg.hi && (key > wlo || key < p.sinks);
-                    st[t][e] = see ? st[t][e] * ks : kNone;
-                }
+                if constexpr (edge) st[t][e] = score_or_none(spread(see[t], e), st[t][e] * ks);
                 mx = fmaxf(mx, st[t][e]);   // a NaN score passes by: it makes the row's sum NaN
             }
         }
@@ -183,10 +180,9 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(AttnArgs p)
             for (int e = 0; e < 16; ++e) {
                 float x;
                 if constexpr (edge) {
-                    const bool see = st[t][e] != kNone;
-                    x = see ? __builtin_amdgcn_exp2f(st[t][e] - mu) : 0.0f;
+                    x = __builtin_amdgcn_exp2f(st[t][e] - mu);     // 0 where masked
                     l += x;
-                    x = see ? x * vs : 0.0f;
+                    x = value_or_zero(spread(see[t], e), x * vs);
                 } else {
                     x = __builtin_amdgcn_exp2f(__builtin_fmaf(st[t][e], scale, -mu));
                     l += x;
@@ -198,7 +194,9 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(AttnArgs p)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const float vs = edge ? 1.0f : e8m0_to_f32(vb[t]);
-            const uint32_t keep = edge ? seen16(rg, ids.of(2 * t + h), t0 + 32 * t + 16 * h) : 0;
+            // what no row sees is no number that may meet a zero
+            const uint32_t keep =
+                edge && ids.of(2 * t + h) >= 0 ? seen16(rg.lo, rg.hi, rg.sinks, t0 + 32 * t + 16 * h) : 0;
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
                 v4i x = *reinterpret_cast<const v4i *>(src + T::K_BYTES + T::value(32 * d + r32, 2 * t + h));
