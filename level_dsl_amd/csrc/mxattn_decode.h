@@ -61,17 +61,16 @@ __global__ __launch_bounds__(THREADS, 2) void decode_kernel(AttnArgs p)
     const Pages &c = p.c;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, g = lane >> 4;
-    int bid = blockIdx.x;
-    const int sp = bid % p.splits;
-    bid /= p.splits;
-    const int rt = bid % p.row_tiles;
-    bid /= p.row_tiles;
-    const int head = bid % c.kv_heads, s = bid / c.kv_heads;
+    uint32_t bid = blockIdx.x;
+    const int sp = (int)(bid % (uint32_t)p.splits);
+    bid /= (uint32_t)p.splits;
+    const int rt = (int)(bid % (uint32_t)p.row_tiles);
+    bid /= (uint32_t)p.row_tiles;
+    const int head = (int)(bid % (uint32_t)c.kv_heads), s = (int)(bid / (uint32_t)c.kv_heads);
 
     const Seq q = cache::sequence(c, s);
-    const int G = p.group;
-    const int64_t rows = (int64_t)q.n * G;
-    const int64_t row0 = (int64_t)rt * ROWS;
+    const uint32_t G = p.group;       // the launch has fewer than 2^24 tiles, so rows fit 32 bits
+    const uint32_t rows = (uint32_t)q.n * G, row0 = (uint32_t)rt * ROWS;
     if (row0 >= rows) return;
     const int pmin = position(q, row0 / G), pmax = position(q, (min(row0 + ROWS, rows) - 1) / G);
     const Range rg = range_of(p, q.ctx, pmin, pmax);
@@ -101,7 +100,7 @@ __global__ __launch_bounds__(THREADS, 2) void decode_kernel(AttnArgs p)
 
     // this lane's column: a row of the tile.  A negative softmax scale goes
     // into the sign of Q, so that the largest product is the largest score.
-    const int64_t row = row0 + r16;
+    const uint32_t row = row0 + r16;
     const bool live = row < rows;
     const int qi = (int)((live ? row : row0) / G), qh = (int)((live ? row : row0) % G);
     const int pos = position(q, qi);

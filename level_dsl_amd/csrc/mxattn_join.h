@@ -23,14 +23,13 @@ __global__ __launch_bounds__(JOIN_THREADS) void join_kernel(AttnArgs p)
     const Pages &c = p.c;
     const int r = blockIdx.x % ROWS;
     const int64_t tile = blockIdx.x / ROWS;
-    int64_t bid = tile;
-    const int rt = (int)(bid % p.row_tiles);
-    bid /= p.row_tiles;
-    const int head = (int)(bid % c.kv_heads), s = (int)(bid / c.kv_heads);
+    uint32_t bid = blockIdx.x / ROWS;
+    const int rt = (int)(bid % (uint32_t)p.row_tiles);
+    bid /= (uint32_t)p.row_tiles;
+    const int head = (int)(bid % (uint32_t)c.kv_heads), s = (int)(bid / (uint32_t)c.kv_heads);
     const Seq q = cache::sequence(c, s);
-    const int G = p.group;
-    const int64_t row = (int64_t)rt * ROWS + r;
-    if (row >= (int64_t)q.n * G) return;
+    const uint32_t G = p.group, row = (uint32_t)rt * ROWS + r;
+    if (row >= (uint32_t)q.n * G) return;
     const float *const part = p.ws + tile * p.splits * PITCH;
 
     __shared__ float weight[MAX_SPLITS], total[2];

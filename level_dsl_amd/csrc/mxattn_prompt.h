@@ -53,25 +53,25 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(AttnArgs p)
     const Pages &c = p.c;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r32 = lane & 31, h = lane >> 5;
-    int64_t bid = blockIdx.x;
-    const int sp = SPLIT ? (int)(bid % p.splits) : 0;
-    if constexpr (SPLIT) bid /= p.splits;
-    const int head = (int)(bid % c.kv_heads);
-    bid /= c.kv_heads;
-    const int s = (int)(bid % c.seqs);
-    const int rt = p.row_tiles - 1 - (int)(bid / c.seqs);
+    uint32_t bid = blockIdx.x;
+    const int sp = SPLIT ? (int)(bid % (uint32_t)p.splits) : 0;
+    if constexpr (SPLIT) bid /= (uint32_t)p.splits;
+    const int head = (int)(bid % (uint32_t)c.kv_heads);
+    bid /= (uint32_t)c.kv_heads;
+    const int s = (int)(bid % (uint32_t)c.seqs);
+    const int rt = p.row_tiles - 1 - (int)(bid / (uint32_t)c.seqs);
 
     const Seq q = cache::sequence(c, s);
-    const int G = p.group;
-    const int64_t rows = (int64_t)q.n * G, row0 = (int64_t)rt * ROWS;
+    const uint32_t G = p.group;       // the launch has fewer than 2^24 tiles, so rows fit 32 bits
+    const uint32_t rows = (uint32_t)q.n * G, row0 = (uint32_t)rt * ROWS;
     if (row0 >= rows) return;
     const Range rg = range_of(p, q.ctx, position(q, row0 / G), position(q, (min(row0 + ROWS, rows) - 1) / G));
     // this wave's rows
-    const int64_t w0 = row0 + wave * WAVE_ROWS;
+    const uint32_t w0 = row0 + wave * WAVE_ROWS;
     const bool any = w0 < rows;
     const int pmin = position(q, (any ? w0 : row0) / G);
     const int pmax = position(q, (any ? min(w0 + WAVE_ROWS, rows) - 1 : row0) / G);
-    const int64_t row = w0 + r32;
+    const uint32_t row = w0 + r32;
     const bool live = row < rows;
     const int qi = (int)((live ? row : row0) / G), qh = (int)((live ? row : row0) % G);
     const int pos = position(q, qi);
