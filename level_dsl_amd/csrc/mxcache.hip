@@ -89,45 +89,9 @@ int64_t rows_of(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads)
     return std::min(b->max_q, b->rows) * (q_heads / c->kv_heads);
 }
 
-// The prompt kernel, or the decode kernel, which reads the keys once for every
-// 16 rows: 8192 keys, 16 sequences, 8 kv heads, dim 128, 32 rows: decode kernel 77
-// us, prompt kernel 98; 48 rows: 109, 114; 72 rows, 1 sequence of 16384: 40, 30.
-bool use_prompt(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads)
+int64_t tiles_of(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads, int rows)
 {
-    return rows_of(c, b, q_heads) > 48;
-}
-
-int tile_rows(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads)
-{
-    return use_prompt(c, b, q_heads) ? mxg::kPromptRows : mxg::kDecodeRows;
-}
-
-int64_t row_tiles(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads)
-{
-    const int r = tile_rows(c, b, q_heads);
-    return (rows_of(c, b, q_heads) + r - 1) / r;
-}
-
-// Splits of the visible keys: enough workgroups for two on each of the 256
-// CUs, but at least four 64-key blocks a split (one per wave of the decode
-// kernel).  More of them cost more than their balance gains (decode, 64
-// sequences of 4097 to 8192 tokens, 8 kv heads: 1 split 160 us, 2: 176, 4:
-// 173).
-int choose_splits(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads, int64_t window)
-{
-    const int64_t tiles = b->seqs * c->kv_heads * row_tiles(c, b, q_heads);
-    const int64_t reach = std::min(b->max_ctx, b->max_pages * c->page_size);
-    const int64_t keys = window && window < reach ? std::min(reach, window + std::min(b->max_q, b->rows)) : reach;
-    const int64_t blocks = (keys + 63) / 64;
-    int64_t s = (512 + tiles - 1) / tiles;
-    s = std::min({s, blocks / 4, (int64_t)mxg::kMaxSplits});
-    return (int)std::max<int64_t>(s, 1);
-}
-
-int64_t workspace(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads, int splits)
-{
-    if (splits == 1) return 0;
-    return b->seqs * c->kv_heads * row_tiles(c, b, q_heads) * splits * tile_rows(c, b, q_heads) * (c->head_dim + 2) * 4;
+    return (rows_of(c, b, q_heads) + rows - 1) / rows;
 }
 
 bool heads_ok(const mxgemm_cache *c, int q_heads)
@@ -135,11 +99,46 @@ bool heads_ok(const mxgemm_cache *c, int q_heads)
     return q_heads >= 1 && q_heads <= 4096 && q_heads % c->kv_heads == 0;
 }
 
-// (splits are taken only while they keep the grid small)
 bool grid_ok(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads)
 {
-    const int64_t t = row_tiles(c, b, q_heads);
+    const int64_t t = tiles_of(c, b, q_heads, mxg::kDecodeRows);
     return t <= kMaxGrid && b->seqs * c->kv_heads <= kMaxGrid / t;
+}
+
+// How a call that passed grid_ok runs.
+struct Plan {
+    bool prompt;
+    int64_t row_tiles, splits, bytes;  // bytes of workspace
+};
+Plan plan_of(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads, int64_t window)
+{
+    const int64_t reach = std::min(b->max_ctx, b->max_pages * c->page_size);
+    const int64_t keys = window && window < reach ? std::min(reach, window + std::min(b->max_q, b->rows)) : reach;
+    const int64_t blocks = (keys + 63) / 64, heads = b->seqs * c->kv_heads;
+    Plan p;
+    // The prompt kernel, or the decode kernel, which reads the keys once for
+    // every 16 rows, but splits the work more finely.  Measured (us, dim 128,
+    // decode / prompt kernel, 16-row tiles times blocks in brackets):
+    //   8 x 64 rows, 512 keys, 4 heads  13.4 / 18.0 [1024]
+    //   1 x 64 x 8 rows, 8192 keys, 8 heads  16.4 / 19.9 [4096]
+    //   2000 x 2 rows, 2000 keys  23.1 / 24.4 [8000]
+    //   4 x 64 rows, 8192 keys, 8 heads  28.3 / 29.8 [16384]
+    //   800 rows, 16384 keys, 2 heads  49.8 / 45.2 [25600]
+    //   16 x 64 rows, 8192 keys, 8 heads  120 / 91 [65536]
+    //   16 x 32 rows, 8192 keys, 8 heads  77 / 98, 48 rows: 109 / 114
+    const int64_t small = tiles_of(c, b, q_heads, mxg::kDecodeRows);
+    p.prompt = rows_of(c, b, q_heads) > 48 && heads * small > 16384 / blocks;
+    const int rows = p.prompt ? mxg::kPromptRows : mxg::kDecodeRows;
+    p.row_tiles = tiles_of(c, b, q_heads, rows);
+    // Splits of the visible keys: enough workgroups for two on each of the 256
+    // CUs, but at least four 64-key blocks a split (one per wave of the decode
+    // kernel).  More of them cost more than their balance gains (decode, 64
+    // sequences of 4097 to 8192 tokens, 8 kv heads: 1 split 160 us, 2: 176, 4:
+    // 173).
+    const int64_t tiles = heads * p.row_tiles;
+    p.splits = std::max<int64_t>(1, std::min({(512 + tiles - 1) / tiles, blocks / 4, (int64_t)mxg::kMaxSplits}));
+    p.bytes = p.splits == 1 ? 0 : tiles * p.splits * rows * (c->head_dim + 2) * 4;
+    return p;
 }
 
 } // namespace
@@ -195,7 +194,7 @@ int64_t mxgemm_cache_attention_workspace(const mxgemm_cache *cache, const mxgemm
     if (check_common(cache, batch) != MXGEMM_OK || !heads_ok(cache, q_heads) || !grid_ok(cache, batch, q_heads) ||
         window < 0)
         return -1;
-    return workspace(cache, batch, q_heads, choose_splits(cache, batch, q_heads, window));
+    return plan_of(cache, batch, q_heads, window).bytes;
 }
 
 int mxgemm_validate_cache_attention(const mxgemm_cache *cache, const mxgemm_batch *batch, const void *Q,
@@ -212,7 +211,7 @@ int mxgemm_validate_cache_attention(const mxgemm_cache *cache, const mxgemm_batc
         o_stride % 8 != 0 || window < 0 || sinks < 0 || (sinks > 0 && window == 0) || !std::isfinite(softmax_scale))
         return MXGEMM_ERR_SHAPE;
     if (((uintptr_t)Q | (uintptr_t)O) & 15u || (uintptr_t)lse & 3u) return MXGEMM_ERR_ALIGN;
-    const int64_t need = ws ? workspace(cache, batch, q_heads, choose_splits(cache, batch, q_heads, window)) : 0;
+    const int64_t need = ws ? plan_of(cache, batch, q_heads, window).bytes : 0;
     if (ws && (((uintptr_t)ws & 255u) || (uint64_t)need > ws_bytes)) return MXGEMM_ERR_WORKSPACE;
     const uint64_t n = code_bytes(cache), ns = (uint64_t)cache->pages * cache->kv_heads;
     const uint64_t qn = ((uint64_t)(batch->rows - 1) * q_stride + width) * 2;
@@ -253,11 +252,12 @@ int mxgemm_cache_attention(mxgemm_t h, const mxgemm_cache *cache, const mxgemm_b
     a.scale_log2 = softmax_scale * 1.4426950408889634f;
     a.window = (int)std::min(window, kMaxInt);
     a.sinks = (int)std::min(sinks, kMaxInt);
-    a.row_tiles = (int)row_tiles(cache, batch, q_heads);
-    a.splits = ws ? choose_splits(cache, batch, q_heads, window) : 1;
+    const Plan plan = plan_of(cache, batch, q_heads, window);
+    a.row_tiles = (int)plan.row_tiles;
+    a.splits = ws ? (int)plan.splits : 1;
     a.ws = (float *)ws;
-    const hipError_t e = use_prompt(cache, batch, q_heads) ? mxg::launch_attn_prompt(cache->head_dim, a, stream)
-                                                           : mxg::launch_attn_decode(cache->head_dim, a, stream);
+    const hipError_t e = plan.prompt ? mxg::launch_attn_prompt(cache->head_dim, a, stream)
+                                     : mxg::launch_attn_decode(cache->head_dim, a, stream);
     return e == hipSuccess ? MXGEMM_OK : MXGEMM_ERR_HIP;
 }
 

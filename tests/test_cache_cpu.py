@@ -104,6 +104,17 @@ def test_workspace_is_what_the_check_asks_for():
             assert vt(dict(args, ws_bytes=n)) == OK and vt(dict(args, ws_bytes=n - 1)) == WS
 
 
+def test_few_rows_want_no_prompt_workspace():
+    """A part of a split holds its row tile's rows: 16 (little work, or at most
+    48 rows) or 128, each of head_dim + 2 floats."""
+    for max_q, max_ctx, rows in ((1, 65536, 16), (24, 65536, 16), (25, 65536, 128), (100, 2048, 16), (2048, 65536, 128)):
+        c, b, _ = structs({"seqs": 1, "rows": 4096, "max_q": max_q, "max_ctx": max_ctx, "max_pages": 4096})
+        n = L.mxgemm_cache_attention_workspace(c, b, 2 * c.kv_heads)
+        tiles = c.kv_heads * -(-2 * max_q // rows)
+        parts = n // (rows * (c.head_dim + 2) * 4)
+        assert n and n % (tiles * rows * (c.head_dim + 2) * 4) == 0 and 2 <= parts // tiles <= 64
+
+
 def test_workspace_of_invalid_arguments():
     c, b, _ = structs({})
     assert L.mxgemm_cache_attention_workspace(c, b, 3) == -1

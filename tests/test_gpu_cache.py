@@ -108,10 +108,12 @@ def test_append_strided_and_edges(gemm):
 
 
 def run_case(gemm, heads, group, dim, page, n, ctx, window=0, sinks=0, seed=5, scale=None, max_ctx=None,
-             spread=1.0, mutate=None, rows_after=2, max_q=None):
+             spread=1.0, mutate=None, rows_after=2, max_q=None, reach=0):
     table, q, cl, pages = ref.batch(len(n), n, ctx, page, seed)
     c = ref.Cache(pages, heads, page, dim, seed)
     fill(c, table, q, cl, seed, spread)
+    if reach > table.shape[1] * page:
+        table = torch.nn.functional.pad(table, (0, reach // page - table.shape[1]), value=-1)
     if mutate:
         mutate(c, table)
     T = sum(n) + rows_after
@@ -169,6 +171,78 @@ def test_attend_few_rows(gemm, heads, group, dim, page, n, ctx, window, sinks):
 @pytest.mark.parametrize("window,sinks", [(0, 0), (50, 4), (130, 0)])
 def test_attend_prompts(gemm, heads, group, dim, page, n, ctx, window, sinks):
     run_case(gemm, heads, group, dim, page, n, ctx, window, sinks)
+
+
+def prompt_launch(heads, group, n, ctx, split):
+    """Arguments of a batch whose stated bounds (rows, new tokens, context) are
+    those of long prompts, so that the kernel for them runs, whole or with its
+    keys split, whatever the real lengths."""
+    wide = len(n) * heads * group              # rows per new token
+    if split:
+        rows = max(8192 // wide, 2100)
+        return {"rows_after": rows, "max_q": rows, "max_ctx": 16384, "reach": 16384}
+    blocks = -(-max(ctx) // 64)
+    rows = 4 * (16 * 16384 // (blocks * wide) + 16)
+    return {"rows_after": rows, "max_q": rows}
+
+
+@pytest.mark.parametrize("heads,group,dim,page,n,ctx", [
+    (1, 1, 64, 16, [100], [100]),
+    (2, 4, 128, 64, [65, 130], [65, 300]),
+    (2, 3, 64, 32, [33, 1, 200], [90, 10, 200]),
+    (1, 8, 128, 128, [40, 129], [700, 129]),
+    (3, 2, 128, 16, [256], [256]),
+    (1, 7, 64, 64, [150], [333]),
+    (1, 3, 128, 64, [5, 3, 0, 70], [2, 0, 40, 40]),
+])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (50, 4), (130, 0), (7, 90), (1, 0)])
+@pytest.mark.parametrize("split", [False, True])
+def test_attend_prompt_kernel(gemm, heads, group, dim, page, n, ctx, window, sinks, split):
+    run_case(gemm, heads, group, dim, page, n, ctx, window, sinks, **prompt_launch(heads, group, n, ctx, split))
+
+
+@pytest.mark.parametrize("split", [False, True])
+def test_attend_prompt_kernel_special(gemm, split):
+    """Pages of NaN, scale bytes far apart, softmax scales that are large, zero
+    and negative, hidden pages."""
+    def nan(c, table):
+        c.ks[int(table[0, 3]), 0] = 255
+        c.vs[int(table[0, 4]), 1] = 255
+
+    def scales(c, table):
+        c.vs[int(table[0, 1]), 0] = 167
+        c.vs[int(table[0, 2]), 0] = 20
+        c.ks[int(table[0, 2]), 0] = 100
+
+    def hide(c, table):
+        table[0, 2] = -1
+        table[0, 5] = 1 << 20
+    for window, sinks in ((0, 0), (20, 17)):
+        run_case(gemm, 2, 2, 64, 16, [100], [120], window, sinks, mutate=nan, **prompt_launch(2, 2, [100], [120], split))
+        run_case(gemm, 2, 2, 64, 16, [100], [120], window, sinks, mutate=hide, **prompt_launch(2, 2, [100], [120], split))
+    one = prompt_launch(1, 2, [50], [100], split)
+    run_case(gemm, 1, 2, 64, 32, [40], [100], mutate=scales, **one)
+    run_case(gemm, 1, 2, 128, 16, [50], [100], scale=40.0, **one)
+    run_case(gemm, 1, 2, 128, 16, [50], [100], scale=0.0, **one)
+    run_case(gemm, 1, 2, 128, 16, [50], [100], scale=-0.3, **one)
+
+
+def test_prompt_kernel_repeats_and_replays(gemm):
+    """The same bits again, also from a captured call between eager ones."""
+    kv, b, Q, out, ls = run_case(gemm, 1, 4, 128, 64, [70, 200], [90, 500], **prompt_launch(1, 4, [70, 200], [90, 500], True))
+    q, dst = Q.to(DEV), torch.zeros_like(out)
+    lse = torch.zeros_like(ls)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kv.attend(b, q, out=dst, lse=lse)
+    for _ in range(3):
+        dst.zero_()
+        graph.replay()
+        o2, l2 = kv.attend(b, q)
+        torch.cuda.synchronize()
+        assert torch.equal(dst[:270], out[:270]) and torch.equal(lse[:270], ls[:270])
+        assert torch.equal(o2[:270], out[:270]) and torch.equal(l2[:270], ls[:270])
 
 
 def test_attend_long_context_splits(gemm):
