@@ -117,26 +117,29 @@ Plan plan_of(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads, int64_t 
     const int64_t blocks = (keys + 63) / 64, heads = b->seqs * c->kv_heads;
     Plan p;
     // The prompt kernel, or the decode kernel, which reads the keys once for
-    // every 16 rows, but splits the work more finely.  Measured (us, dim 128,
-    // decode / prompt kernel, 16-row tiles times blocks in brackets):
-    //   8 x 64 rows, 512 keys, 4 heads  13.4 / 18.0 [1024]
-    //   1 x 64 x 8 rows, 8192 keys, 8 heads  16.4 / 19.9 [4096]
-    //   2000 x 2 rows, 2000 keys  23.1 / 24.4 [8000]
-    //   4 x 64 rows, 8192 keys, 8 heads  28.3 / 29.8 [16384]
-    //   800 rows, 16384 keys, 2 heads  49.8 / 45.2 [25600]
-    //   16 x 64 rows, 8192 keys, 8 heads  120 / 91 [65536]
+    // every 16 rows, but splits the work more finely: by the 16-row tiles times
+    // the blocks that a row sees on average.  Measured (us, dim 128, decode /
+    // prompt kernel, that product in brackets):
+    //   8 x 64 rows, 512 keys, 4 heads  13 / 18 [1000]      64 x 8 rows, 8192 keys, 8 heads  28 / 30 [16400]
+    //   4096 rows, 1024 keys, 2 heads  13 / 29 [4100]       2 x 2048 rows, 4096 keys, 2 heads  38 / 41 [30700]
+    //   4096 rows, 1024 keys, 8 heads  40 / 59 [16400]      800 rows, 16384 keys, 2 heads  39 / 37 [25500]
+    //   4 x 512 rows, 2048 keys, 8 heads  37 / 47 [28700]   4 x 96 rows, 8192 keys, 8 heads  45 / 33 [24600]
+    //   2048 rows, 8192 keys, 8 heads  133 / 97 [127000]    16 x 64 rows, 8192 keys, 8 heads  119 / 91 [65500]
     //   16 x 32 rows, 8192 keys, 8 heads  77 / 98, 48 rows: 109 / 114
     const int64_t small = tiles_of(c, b, q_heads, mxg::kDecodeRows);
-    p.prompt = rows_of(c, b, q_heads) > 48 && heads * small > 16384 / blocks;
+    const int64_t seen = window && window < reach ? blocks : (reach - std::min(std::min(b->max_q, b->rows), reach) / 2 + 63) / 64;
+    p.prompt = rows_of(c, b, q_heads) > 48 && heads * small > 24000 / seen;
     const int rows = p.prompt ? mxg::kPromptRows : mxg::kDecodeRows;
     p.row_tiles = tiles_of(c, b, q_heads, rows);
-    // Splits of the visible keys: enough workgroups for two on each of the 256
-    // CUs, but at least four 64-key blocks a split (one per wave of the decode
-    // kernel).  More of them cost more than their balance gains (decode, 64
+    // Splits of the visible keys: as many as make at most two workgroups for
+    // each of the 256 CUs, which is what they hold at dim 128 (4 x 96 rows, 8192
+    // keys, 8 heads, decode kernel: 384 workgroups 45 us, 576: 65 us), with at
+    // least four 64-key blocks a split, one per wave of the decode kernel.  More
+    // than one round of them costs more than its balance gains (decode, 64
     // sequences of 4097 to 8192 tokens, 8 kv heads: 1 split 160 us, 2: 176, 4:
     // 173).
     const int64_t tiles = heads * p.row_tiles;
-    p.splits = std::max<int64_t>(1, std::min({(512 + tiles - 1) / tiles, blocks / 4, (int64_t)mxg::kMaxSplits}));
+    p.splits = std::max<int64_t>(1, std::min({512 / tiles, blocks / 4, (int64_t)mxg::kMaxSplits}));
     p.bytes = p.splits == 1 ? 0 : tiles * p.splits * rows * (c->head_dim + 2) * 4;
     return p;
 }

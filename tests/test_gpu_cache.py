@@ -179,7 +179,7 @@ def prompt_launch(heads, group, n, ctx, split):
     keys split, whatever the real lengths."""
     wide = len(n) * heads * group              # rows per new token
     if split:
-        rows = max(8192 // wide, 2100)
+        rows = min(max(16000 // wide, 2000), 32000 // wide)     # at most 256 tiles of 128 rows
         return {"rows_after": rows, "max_q": rows, "max_ctx": 16384, "reach": 16384}
     blocks = -(-max(ctx) // 64)
     rows = 4 * (16 * 16384 // (blocks * wide) + 16)
