@@ -21,7 +21,7 @@
 // otherwise).  The longest rows' workgroups start first.  Few rows over many
 // keys are split along the keys.
 //
-// 2 x 2048 rows over 8192 keys, 32 / 8 heads, dim 128: 456 us, 960 TFLOP/s.
+// 2 x 2048 rows over 8192 keys, 32 / 8 heads, dim 128: 443 us, 985 TFLOP/s.
 // The SIMDs are busy issuing: per wave and block 32 MFMAs (1024 cycles) and
 // about 280 other vector instructions (1300 cycles), 128 of them the widening.
 // Widening once for all four waves through LDS (540 us) and running the first

@@ -26,6 +26,13 @@
 // has a scale per row), loaded a window ahead into registers and turned into
 // [stage][row] order in LDS, so that a lane's rows are one conflict-free
 // read.  With 128 x 128 blocks, B's scale is one scalar per wave and stage.
+//
+// Measured (e4m3): native, 8192^3, bf16 out 455-485 us (2.3-2.4 PFLOP/s): one FMA
+// per output and stage beside the MFMAs (128 against 32 of 16 cycles, per
+// wave), at the clock that this load is held to.  Exact, 4096^3, bf16 out 119 us
+// (1.15 PFLOP/s); with a scale per row of B and fp32 out 135 us: the widening
+// (128 conversions) and the scales' 64 or 128 instructions beside 64 MFMAs of 16
+// cycles.
 #pragma once
 
 #include "mxblock.h"

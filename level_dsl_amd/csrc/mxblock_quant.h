@@ -10,7 +10,9 @@
 // through LDS.  The transpose's codes go through LDS so that they too are
 // stored as whole 128-byte rows.
 //
-// Bound by HBM: one read of X, one write of each code.
+// Bound by HBM: one read of X, one write of each code.  28672 x 8192 fp32 in 128 x
+// 128 blocks with the transpose: 269 us, 5.25 TB/s; 4095 x 8192 bf16 rows and
+// columns: 31 us (two sets of codes, a division per row, column and block).
 #pragma once
 
 #include "mxblock.h"
