@@ -394,6 +394,8 @@ class Gemm:
 
     def __init__(self):
         self.h = mxgemm_create()
+        self.lib = load_library()
+        self.device = torch.cuda.current_device()   # the handle's
         self.scale_layout = MXGEMM_SCALES_ROW_MAJOR
 
     def close(self):
@@ -531,12 +533,17 @@ class Gemm:
         if A.dtype != torch.uint8 or B.dtype != torch.uint8 or A_scale.dtype != torch.float32 or \
                 B_scale.dtype != torch.float32:
             raise ValueError("codes must be uint8 and scales float32")
-        _same_device(A, A_scale, B, B_scale, C)
+        _on_device(self.device, A, A_scale, B, B_scale, C)
         if not (A.is_contiguous() and B.is_contiguous() and A_scale.is_contiguous() and
                 B_scale.is_contiguous() and C.is_contiguous()):
             raise ValueError("all operands must be contiguous")
-        mxgemm_run_block128(self.h, A, A_scale, fmtA, B, B_scale, fmtB, 128 if sb[0] == nb else 1, C,
-                            M, N, K, use_acc, MXGEMM_OUT_F32 if f32 else MXGEMM_OUT_BF16, stream)
+        # the library at once: a call of the wrapper costs a microsecond more
+        rc = self.lib.mxgemm_run_block128(
+            self.h, A.data_ptr(), A_scale.data_ptr(), fmtA, B.data_ptr(), B_scale.data_ptr(), fmtB,
+            128 if sb[0] == nb else 1, C.data_ptr(), M, N, K, 1 if use_acc else 0,
+            MXGEMM_OUT_F32 if f32 else MXGEMM_OUT_BF16, _stream_on(stream, self.device))
+        if rc:
+            _check(rc, "mxgemm_run_block128")
         return C
 
     def quantize_block128(self, X, fmt, rows=1, normal=True, transposed=False, stream=None):
@@ -544,8 +551,9 @@ class Gemm:
         blocks of `rows` (1 or 128) x 128: (codes (R, K), scales) if `normal`,
         then (codes of the transpose (K, R rounded up to 16), their scales) if
         `transposed`."""
-        if X.dim() != 2 or not X.is_contiguous() or X.device.type != "cuda":
+        if X.dim() != 2 or not X.is_contiguous():
             raise ValueError("X must be a contiguous 2-D device tensor")
+        _on_device(self.device, X)
         if X.dtype not in (torch.float32, torch.bfloat16):
             raise ValueError("X must be float32 or bfloat16")
         if rows not in (1, 128):
@@ -554,17 +562,34 @@ class Gemm:
             raise ValueError("nothing to compute: normal and transposed are both off")
         R, K = X.shape
         kb, rb = (K + 127) // 128, (R + 127) // 128
-        dev, c, sc, ct, st = X.device, None, None, None, None
         with _on_stream(stream):
             if normal:
-                c = torch.empty((R, K), dtype=torch.uint8, device=dev)
-                sc = torch.empty((R if rows == 1 else rb, kb), dtype=torch.float32, device=dev)
+                c = X.new_empty((R, K), dtype=torch.uint8)
+                sc = X.new_empty((R if rows == 1 else rb, kb), dtype=torch.float32)
             if transposed:
-                ct = torch.empty((K, (R + 15) // 16 * 16), dtype=torch.uint8, device=dev)
-                st = torch.empty((K if rows == 1 else kb, rb), dtype=torch.float32, device=dev)
-        mxgemm_quantize_block128(self.h, X, MXGEMM_X_F32 if X.dtype == torch.float32 else MXGEMM_X_BF16,
-                                 R, K, rows, fmt, c, sc, ct, st, stream)
+                ct = X.new_empty((K, (R + 15) // 16 * 16), dtype=torch.uint8)
+                st = X.new_empty((K if rows == 1 else kb, rb), dtype=torch.float32)
+        rc = self.lib.mxgemm_quantize_block128(
+            self.h, X.data_ptr(), MXGEMM_X_F32 if X.dtype == torch.float32 else MXGEMM_X_BF16, R, K, rows, fmt,
+            c.data_ptr() if normal else None, sc.data_ptr() if normal else None,
+            ct.data_ptr() if transposed else None, st.data_ptr() if transposed else None,
+            _stream_on(stream, self.device))
+        if rc:
+            _check(rc, "mxgemm_quantize_block128")
         return (c, sc) if not transposed else (c, sc, ct, st) if normal else (ct, st)
+
+
+def _on_device(device, *tensors):
+    for t in tensors:
+        if t.get_device() != device:     # -1 on the host
+            raise ValueError(f"all tensors must be on the handle's GPU (cuda:{device})")
+
+
+def _stream_on(stream, device) -> int:
+    """_stream for a call whose tensors are on `device`."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device)
+    return _stream(stream)
 
 
 def _same_device(*tensors):
@@ -647,20 +672,20 @@ class KVCache:
                 v_scales.shape != (pages, heads):
             raise ValueError("v_codes must be (pages, kv_heads, head_dim, page_size), the scales "
                              "(pages, kv_heads)")
-        _same_device(k_codes, k_scales, v_codes, v_scales)
+        _on_device(gemm.device, k_codes, k_scales, v_codes, v_scales)
         self.tensors = (k_codes, k_scales, v_codes, v_scales)
         for t in self.tensors:
             if t.dtype != torch.uint8 or not t.is_contiguous():
                 raise ValueError("codes and scales must be contiguous uint8")
-        self.gemm, self.device = gemm, k_codes.get_device()
+        self.gemm, self.device = gemm, gemm.device
         self.page_size, self.kv_heads, self.head_dim = page, heads, dim
         self.struct = CacheStruct(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                                   v_scales.data_ptr(), pages, page, heads, dim)
 
     @classmethod
-    def empty(cls, gemm: Gemm, pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda:0"):
-        """A cache of new tensors (zeros)."""
-        z = lambda *shape: torch.zeros(shape, dtype=torch.uint8, device=device)
+    def empty(cls, gemm: Gemm, pages: int, page_size: int, kv_heads: int, head_dim: int):
+        """A cache of new tensors (zeros) on the handle's GPU."""
+        z = lambda *shape: torch.zeros(shape, dtype=torch.uint8, device=f"cuda:{gemm.device}")
         return cls(gemm, z(pages, kv_heads, page_size, head_dim), z(pages, kv_heads),
                    z(pages, kv_heads, head_dim, page_size), z(pages, kv_heads))
 
@@ -678,8 +703,13 @@ class KVCache:
             raise ValueError("K, V and the cache must be on one GPU")
         if K.shape[0] == 0:
             return
-        mxgemm_cache_append(self.gemm.h, self.struct, batch.struct(self, K.shape[0]), K, V,
-                            MXGEMM_X_F32 if K.dtype == torch.float32 else MXGEMM_X_BF16, stride, stream)
+        b = batch.struct(self, K.shape[0])
+        rc = self.gemm.lib.mxgemm_cache_append(
+            self.gemm.h, ctypes.addressof(self.struct), ctypes.addressof(b), K.data_ptr(), V.data_ptr(),
+            MXGEMM_X_F32 if K.dtype == torch.float32 else MXGEMM_X_BF16, stride,
+            _stream_on(stream, self.device))
+        if rc:
+            _check(rc, "mxgemm_cache_append")
 
     def attend(self, batch: Batch, Q, scale: float = None, window: int = 0, sinks: int = 0, out=None,
                lse=None, stream=None):
@@ -695,14 +725,14 @@ class KVCache:
         q_stride = _token_stride(Q, heads, self.head_dim, "Q")
         with _on_stream(stream):
             if out is None:
-                out = torch.empty((T, heads, dim), dtype=torch.bfloat16, device=Q.device)
+                out = Q.new_empty((T, heads, dim))
                 o_stride = heads * dim
             else:
                 if out.shape != Q.shape or out.dtype != torch.bfloat16 or out.get_device() != self.device:
                     raise ValueError("out must be bfloat16 like Q")
                 o_stride = _token_stride(out, heads, dim, "out")
             if lse is None:
-                lse = torch.empty((T, heads), dtype=torch.float32, device=Q.device)
+                lse = Q.new_empty((T, heads), dtype=torch.float32)
             elif lse.shape != (T, heads) or lse.dtype != torch.float32 or lse.get_device() != self.device or \
                     not lse.is_contiguous():
                 raise ValueError("lse must be a contiguous (tokens, q_heads) float32")
@@ -711,9 +741,13 @@ class KVCache:
             b = batch.struct(self, T)
             # a workspace of its own for each call: calls on several streams and
             # captured graphs share none
-            n = mxgemm_cache_attention_workspace(self.struct, b, heads, window)
-            ws = torch.empty(n, dtype=torch.uint8, device=Q.device) if n > 0 else None
-            mxgemm_cache_attention(self.gemm.h, self.struct, b, Q, heads, q_stride,
-                                   self.head_dim ** -0.5 if scale is None else scale, window, sinks, out,
-                                   o_stride, lse, ws, max(n, 0), stream)
+            lib, at, b_at = self.gemm.lib, ctypes.addressof(self.struct), ctypes.addressof(b)
+            n = max(lib.mxgemm_cache_attention_workspace(at, b_at, heads, window), 0)
+            ws = Q.new_empty((n,), dtype=torch.uint8) if n else None
+            rc = lib.mxgemm_cache_attention(
+                self.gemm.h, at, b_at, Q.data_ptr(), heads, q_stride,
+                self.head_dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), o_stride,
+                lse.data_ptr(), ws.data_ptr() if n else None, n, _stream_on(stream, self.device))
+            if rc:
+                _check(rc, "mxgemm_cache_attention")
         return out, lse

@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 import level_dsl_amd as L
 
@@ -131,3 +132,22 @@ def test_bad_handle_launches_nothing():
     pc, pb = ctypes.addressof(c), ctypes.addressof(b)
     assert lib.mxgemm_cache_append(None, pc, pb, K, V, 1, 256, None) == bad
     assert lib.mxgemm_cache_attention(None, pc, pb, Q, 8, 1024, 0.1, 0, 0, O, 1024, LSE, None, 0, None) == bad
+
+
+class OtherGpu:
+    """A handle of a GPU that none of the tensors is on; a call that got past
+    the checks would have no library to go to."""
+    h, lib, device = None, None, 1
+
+
+def test_tensors_elsewhere_are_refused():
+    u8 = torch.zeros((4, 128), dtype=torch.uint8)
+    f = torch.ones((4, 1))
+    with pytest.raises(ValueError, match="GPU"):
+        L.Gemm.block128(OtherGpu, u8, f, 0, u8.clone(), f, 0, torch.zeros((4, 4)))
+    with pytest.raises(ValueError, match="GPU"):
+        L.Gemm.quantize_block128(OtherGpu, torch.zeros((4, 128)), 0)
+    codes = torch.zeros((2, 1, 16, 64), dtype=torch.uint8)
+    scales = torch.zeros((2, 1), dtype=torch.uint8)
+    with pytest.raises(ValueError, match="GPU"):
+        L.KVCache(OtherGpu, codes, scales, codes.transpose(2, 3).contiguous(), scales.clone())
