@@ -77,15 +77,60 @@ __global__ __launch_bounds__(JOIN_THREADS) void join_kernel(AttnArgs p, uint32_t
     if (tid == 0 && p.lse) p.lse[token * p.q_heads + h] = (total[0] + __builtin_log2f(l)) * kLn2;
 }
 
+// The same for few splits: a lane group of D / 4 takes a row of its own and adds
+// its splits in turn, 256 / (D / 4) rows a workgroup.
+template <int D, int ROWS>
+__global__ __launch_bounds__(JOIN_THREADS) void join_rows_kernel(AttnArgs p, uint32_t used)
+{
+    constexpr int LANES = D / 4, GROUPS = JOIN_THREADS / LANES;
+    constexpr int64_t PITCH = ROWS * (D + 2);
+    const Pages &c = p.c;
+    const uint32_t per = (used + GROUPS - 1) / GROUPS;
+    const int r = (int)(blockIdx.x % per) * GROUPS + (int)(threadIdx.x / LANES);
+    uint32_t bid = blockIdx.x / per;
+    const int64_t tile = bid;
+    const int rt = (int)(bid % (uint32_t)p.row_tiles);
+    bid /= (uint32_t)p.row_tiles;
+    const int head = (int)(bid % (uint32_t)c.kv_heads), s = (int)(bid / (uint32_t)c.kv_heads);
+    const Seq q = cache::sequence(c, s);
+    const uint32_t G = p.group, row = (uint32_t)rt * ROWS + r;
+    if (r >= ROWS || row >= (uint32_t)q.n * G) return;
+    const float *const part = p.ws + tile * p.splits * PITCH;
+    const int d4 = threadIdx.x % LANES;
+    float mt = kNone;
+    for (int k = 0; k < p.splits; ++k) mt = fmaxf(mt, part[k * PITCH + ROWS * D + r]);
+    const float mu = mt == kNone ? 0.0f : mt;
+    float l = 0.0f;
+    v4f v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = 0; k < p.splits; ++k) {
+        const float *const x = part + k * PITCH;
+        const float w = __builtin_amdgcn_exp2f(x[ROWS * D + r] - mu);
+        l += x[ROWS * D + ROWS + r] * w;
+        v += *reinterpret_cast<const v4f *>(x + r * D + 4 * d4) * w;
+    }
+    v *= l == 0.0f ? 0.0f : 1.0f / l;
+    const int64_t token = q.q0 + row / G;
+    const int h = head * G + (int)(row % G);
+    *reinterpret_cast<v2i *>(p.O + token * p.o_stride + (int64_t)h * D + 4 * d4) =
+        v2i{(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3])};
+    if (d4 == 0 && p.lse) p.lse[token * p.q_heads + h] = (mu + __builtin_log2f(l)) * kLn2;
+}
+
 // Joins tiles * a.splits parts of row tiles of ROWS.
 template <int D, int ROWS>
 inline hipError_t launch_join(const AttnArgs &a, int64_t tiles, hipStream_t s)
 {
     static_assert(MAX_SPLITS == kMaxSplits, "host and kernel agree");
-    // rows of a tile that can exist: a workgroup for each of them (32 sequences of
-    // one token, 4 heads of 8 groups, 2 splits: 5 us, 6.6 with 16 a tile)
+    constexpr int GROUPS = JOIN_THREADS / (D / 4);
+    // rows of a tile that can exist
     const int64_t used = std::min((int64_t)ROWS, (int64_t)a.c.max_q * a.group);
-    hipLaunchKernelGGL((join_kernel<D, ROWS>), dim3((unsigned)(tiles * used)), dim3(JOIN_THREADS), 0, s, a, (uint32_t)used);
+    if (a.splits <= GROUPS)
+        hipLaunchKernelGGL((join_rows_kernel<D, ROWS>), dim3((unsigned)(tiles * ((used + GROUPS - 1) / GROUPS))),
+                           dim3(JOIN_THREADS), 0, s, a, (uint32_t)used);
+    else
+        hipLaunchKernelGGL((join_kernel<D, ROWS>), dim3((unsigned)(tiles * used)), dim3(JOIN_THREADS), 0, s, a,
+                           (uint32_t)used);
     return hipGetLastError();
 }
 
