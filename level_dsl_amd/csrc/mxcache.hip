@@ -113,22 +113,29 @@ struct Plan {
 Plan plan_of(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads, int64_t window)
 {
     const int64_t reach = std::min(b->max_ctx, b->max_pages * c->page_size);
-    const int64_t keys = window && window < reach ? std::min(reach, window + std::min(b->max_q, b->rows)) : reach;
-    const int64_t blocks = (keys + 63) / 64, heads = b->seqs * c->kv_heads;
+    const int64_t heads = b->seqs * c->kv_heads, tokens = std::min(b->max_q, b->rows);
+    const bool windowed = window > 0 && window < reach;
+    // blocks that a tile of so many rows sees at most (but for sinks)
+    auto blocks_of = [&](int rows) {
+        const int64_t own = std::min(tokens, (int64_t)rows * c->kv_heads / q_heads + 1);
+        return ((windowed ? std::min(reach, window + own) : reach) + 63) / 64;
+    };
     Plan p;
     // The prompt kernel, or the decode kernel, which reads the keys once for
     // every 16 rows, but splits the work more finely: by the 16-row tiles times
-    // the blocks that a row sees on average.  Measured (us, dim 128, decode /
-    // prompt kernel, that product in brackets):
-    //   8 x 64 rows, 512 keys, 4 heads  13 / 18 [1000]      64 x 8 rows, 8192 keys, 8 heads  28 / 30 [16400]
-    //   4096 rows, 1024 keys, 2 heads  13 / 29 [4100]       2 x 2048 rows, 4096 keys, 2 heads  38 / 41 [30700]
-    //   4096 rows, 1024 keys, 8 heads  40 / 59 [16400]      800 rows, 16384 keys, 2 heads  39 / 37 [25500]
-    //   4 x 512 rows, 2048 keys, 8 heads  37 / 47 [28700]   4 x 96 rows, 8192 keys, 8 heads  45 / 33 [24600]
-    //   2048 rows, 8192 keys, 8 heads  133 / 97 [127000]    16 x 64 rows, 8192 keys, 8 heads  119 / 91 [65500]
+    // the blocks that a row sees on average, and for many tiles of few blocks,
+    // where the decode kernel's fixed work counts, by the tiles alone.  Measured
+    // (us, dim 128, decode / prompt kernel, tiles x blocks in brackets):
+    //   64 x 8 rows, 512 keys, 4 heads  13 / 18 [128 x 8]          4096 rows, 1024 keys, 2 heads  13 / 29 [512 x 8]
+    //   6000 rows, 1500 keys, 2 heads  25 / 31 [750 x 12]          4 x 64 rows, 8192 keys, 8 heads  28 / 30 [128 x 128]
+    //   2 x 2048 rows, 4096 keys, 2 heads  36 / 39 [512 x 60]      4 x 512 rows, 2048 keys, 8 heads  32 / 35 [1024 x 28]
+    //   4 x 96 rows, 8192 keys, 8 heads  43 / 32 [192 x 128]       16 x 64 rows, 8192 keys, 8 heads  122 / 80 [512 x 128]
+    //   8 x 128 rows, 128 keys, 8 heads  8.8 / 9.7 [512 x 1]       64 x 80 rows, 40 keys, 8 heads  29 / 12 [2560 x 1]
+    //   49 x 72 rows, 72 keys, 4 heads  14 / 9.2 [980 x 1]         5 x 916 rows, 229 keys, 8 heads  24 / 16 [2320 x 2]
     //   16 x 32 rows, 8192 keys, 8 heads  77 / 98, 48 rows: 109 / 114
     const int64_t small = tiles_of(c, b, q_heads, mxg::kDecodeRows);
-    const int64_t seen = window && window < reach ? blocks : (reach - std::min(std::min(b->max_q, b->rows), reach) / 2 + 63) / 64;
-    p.prompt = rows_of(c, b, q_heads) > 48 && heads * small > 24000 / seen;
+    const int64_t seen = windowed ? blocks_of(mxg::kDecodeRows) : (reach - std::min(tokens, reach) / 2 + 63) / 64;
+    p.prompt = rows_of(c, b, q_heads) > 48 && (heads * small > 24000 / seen || (heads * small > 900 && seen <= 8));
     const int rows = p.prompt ? mxg::kPromptRows : mxg::kDecodeRows;
     p.row_tiles = tiles_of(c, b, q_heads, rows);
     // Splits of the visible keys: as many as make at most two workgroups for
@@ -139,7 +146,7 @@ Plan plan_of(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads, int64_t 
     // sequences of 4097 to 8192 tokens, 8 kv heads: 1 split 160 us, 2: 176, 4:
     // 173).
     const int64_t tiles = heads * p.row_tiles;
-    p.splits = std::max<int64_t>(1, std::min({512 / tiles, blocks / 4, (int64_t)mxg::kMaxSplits}));
+    p.splits = std::max<int64_t>(1, std::min({512 / tiles, blocks_of(rows) / 4, (int64_t)mxg::kMaxSplits}));
     p.bytes = p.splits == 1 ? 0 : tiles * p.splits * rows * (c->head_dim + 2) * 4;
     return p;
 }

@@ -201,6 +201,13 @@ def test_attend_prompt_kernel(gemm, heads, group, dim, page, n, ctx, window, sin
     run_case(gemm, heads, group, dim, page, n, ctx, window, sinks, **prompt_launch(heads, group, n, ctx, split))
 
 
+@pytest.mark.parametrize("dim,page", [(128, 64), (64, 16)])
+@pytest.mark.parametrize("sinks", [0, 70])
+def test_attend_prompt_kernel_window_split(gemm, dim, page, sinks):
+    """A window long enough for its keys to be split."""
+    run_case(gemm, 1, 4, dim, page, [150], [1500], 700, sinks, rows_after=8150, max_q=8150)
+
+
 @pytest.mark.parametrize("split", [False, True])
 def test_attend_prompt_kernel_special(gemm, split):
     """Pages of NaN, scale bytes far apart, softmax scales that are large, zero
