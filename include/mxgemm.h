@@ -402,8 +402,9 @@ int mxgemm_quantize(mxgemm_t h, const void *X, int x_dtype, int64_t R, int64_t K
  *   B        N x K codes, K contiguous; Bs  ceil(N / b_rows) x KB fp32;
  *   C        M x N fp32 or bf16, as for mxgemm_run.
  * K is a multiple of 16 (the last block may be short).  The product of two
- * scales is taken first, in fp32: where it overflows, the outputs of that row
- * and column are infinite or NaN.
+ * scales is taken first, in fp32, by every kernel: where it overflows, the
+ * output is infinite or NaN; where it falls below 2^-126, it loses bits, and
+ * the output with it.  Elsewhere the bound below holds, whatever the scales.
  *
  * Arithmetic, by the handle's variant (mxgemm_set_variant):
  *   AUTO, LARGE, SKINNY   exact: the codes are widened to bf16 (exact), each

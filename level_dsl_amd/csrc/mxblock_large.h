@@ -162,12 +162,14 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(block::Args p)
                 sn[j & 1] = *reinterpret_cast<const v4f *>(reinterpret_cast<const uint8_t *>(scale_b) + stage_off + sn_off +
                                                            j * 64);
         };
+        // the two scales first: a block's sum times one of them may leave the fp32
+        // range where their product does not
         auto join = [&](int j, const v4f (&t)[MT]) MXG_INLINE {
             if constexpr (ROWS_B == 1) {
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[i][j][e] += t[i][e] * s[i] * sn[j & 1][e];
+                    for (int e = 0; e < 4; ++e) acc[i][j][e] += t[i][e] * (s[i] * sn[j & 1][e]);
             } else {
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
