@@ -543,7 +543,9 @@ int mxgemm_cache_append(mxgemm_t h, const mxgemm_cache *cache, const mxgemm_batc
  * for scale bytes 10 .. 246 (below, magnitudes under 2^-133 may be lost, above,
  * those from 2^128 are infinite); scores, maximum, sum and output are fp32; the
  * probabilities are rounded to bf16 (2^-8 relative at most) as the second
- * product's operand, not in the sum.
+ * product's operand, not in the sum.  They are divided by their sum at the end
+ * and reach 2^8 before: of each key 2^-116 of the value may be lost, and outputs
+ * may overflow where 2^8 |v| summed over the visible keys passes 2^128.
  *
  * ws: mxgemm_cache_attention_workspace bytes, 256-byte aligned, lets few rows
  * over long contexts be split over the GPU; NULL / 0 never splits.  Calls

@@ -422,7 +422,8 @@ __device__ __forceinline__ void clamp_scale(uint32_t s, float &dec, int &rem, fl
 // times `scale`, rounded to nearest even (v_cvt_scalef32_pk_bf16_fp8 / _bf8).
 // For every code and every power-of-two scale 2^-127..2^127 this was checked
 // on the device to equal round-to-nearest-even of the exact product; it is
-// exact whenever that product is a bf16 number.
+// exact whenever that product is a bf16 number.  A NaN scale gives NaN for
+// every code.
 template <int F, bool HI>
 __device__ __forceinline__ v2bf cvt2(uint32_t w, float scale)
 {

@@ -493,3 +493,129 @@ def test_two_streams(gemm):
     for x, y in got:
         assert torch.equal(x[0][:2], a[3][:2]) and torch.equal(y[0][:2], c[3][:2])
         assert torch.equal(x[1][:2], a[4][:2]) and torch.equal(y[1][:2], c[4][:2])
+
+
+def run_prompt_both(gemm, heads, group, dim, page, n, ctx, window=0, sinks=0, seed=5, scale=None, mutate=None):
+    """The prompt kernel with its keys split, then whole, against the definition.
+    The stated bounds (new tokens, context) are those of long prompts; that
+    the prompt kernel is the one they choose is read off the workspace, whose
+    parts are tiles of 128 rows (of 16 in the other kernel).  The unsplit run
+    is the same call without a workspace."""
+    table, q, cl, pages = ref.batch(len(n), n, ctx, page, seed)
+    c = ref.Cache(pages, heads, page, dim, seed)
+    fill(c, table, q, cl, seed)
+    reach = 16384
+    table = torch.nn.functional.pad(table, (0, reach // page - table.shape[1]), value=-1)
+    if mutate:
+        mutate(c, table)
+    Hq, wide = heads * group, len(n) * heads
+    rows = 250 // wide * 128 // group - 11
+    T = max(rows, sum(n) + 2)
+    Q = rand((T, Hq, dim), seed + 9).bfloat16()
+    used = sum(n) + 2                        # the rows past the last sequence's need no reference
+    sc = dim ** -0.5 if scale is None else scale
+    O, lse, to, tl = ref.attend(c, table, q, cl, Q[:used], sc, window, sinks)
+    to += lost(c, table, q, cl, used, group)
+    kv = upload(gemm, c)
+    b = L.Batch(table.to(DEV), q.to(DEV), cl.to(DEV), max_q=rows, max_ctx=reach)
+    st = b.struct(kv, T)
+    part = wide * -(-rows * group // 128) * 128 * (dim + 2) * 4
+    nbytes = L.mxgemm_cache_attention_workspace(kv.struct, st, Hq, window)
+    assert 0 < rows * group % 128 <= 112
+    assert nbytes >= 2 * part and nbytes % part == 0, "not the prompt kernel's workspace for two splits or more"
+    Qd = Q.to(DEV)
+    for split in (True, False):
+        out = torch.full((T, Hq, dim), 3.0, dtype=torch.bfloat16, device=DEV)
+        ls = torch.full((T, Hq), 3.0, device=DEV)
+        if split:
+            kv.attend(b, Qd, scale=scale, window=window, sinks=sinks, out=out, lse=ls)
+        else:
+            L.mxgemm_cache_attention(gemm.h, kv.struct, st, Qd, Hq, Hq * dim, sc, window, sinks, out, Hq * dim, ls,
+                                     None, 0)
+        torch.cuda.synchronize()
+        assert (out[used:] == 3.0).all() and (ls[used:] == 3.0).all()
+        compare(out[:used], ls[:used], O, lse, to, tl, sum(n))
+
+
+def lost(c, table, q_start, ctx_len, T, group):
+    """What a row's output may lose where probabilities leave the fp32 range,
+    which counts beside values that differ by 2^100 or more.  A probability is
+    2^(x - m) with m at most the row's largest score, and is lost below 2^-126.  It
+    may be 2^8, and is scaled down when m grows and when the splits' sums meet, by
+    factors that are lost below 2^-126 too: at most 2^8 2^-126 of a value, three
+    times.  The sum that it is divided by is at least 1, the largest score's own
+    term.  Together under 2^-116 of the sum of the values' magnitudes (those in
+    slots behind the context are counted along: a bound still)."""
+    t = torch.zeros((T, c.heads * group, c.dim), dtype=torch.float64)
+    for s in range(table.shape[0]):
+        ids = table[s, :-(-int(ctx_len[s]) // c.page)].long()
+        ids = ids[(ids >= 0) & (ids < c.pages)]
+        for h in range(c.heads):
+            v = c.v[ids, h].view(ref.E4).double() * ref.pow2(c.vs[ids, h])[:, None, None]
+            t[int(q_start[s]):int(q_start[s + 1]), h * group:(h + 1) * group] = \
+                2.0 ** -116 * v.nan_to_num(0.0).abs().sum((0, 2))
+    return t
+
+
+def at_tokens(table, seq, *tokens, page):
+    return [int(table[seq, t // page]) for t in tokens]
+
+
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 64), (128, 16), (64, 128)])
+@pytest.mark.parametrize("n,ctx", [([100, 33], [420, 1000]), ([129], [519])])
+def test_attend_prompt_whole_blocks(gemm, dim, page, n, ctx):
+    run_prompt_both(gemm, 2, 3, dim, page, n, ctx)
+
+
+# a window that leaves whole blocks between its edges, alone and with sinks
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("sinks", [0, 3, 200])
+def test_attend_prompt_window_blocks(gemm, dim, page, sinks):
+    run_prompt_both(gemm, 2, 3, dim, page, [150, 1], [2300, 1700], 1600, sinks)
+
+
+# tokens of interior blocks, which every row of the prompt sees whole (first
+# row at 320 without a window; 880 to 2200 and the sinks with it), and of a
+# block that the window's lower edge cuts
+@pytest.mark.parametrize("dim,page", [(64, 16), (64, 32), (128, 64), (128, 128)])
+@pytest.mark.parametrize("window,sinks,n,ctx,token", [(0, 0, 100, 420, 70), (0, 0, 100, 420, 200),
+                                                     (1500, 130, 100, 2300, 1100), (1500, 130, 100, 2300, 10),
+                                                     (1500, 0, 100, 2300, 740)])
+def test_attend_prompt_interior_special(gemm, dim, page, window, sinks, n, ctx, token):
+    """Pages inside the unmasked blocks of long prompts: a byte of NaN for keys
+    (head 0) or values (head 1) makes NaN of exactly the rows and head that see
+    it; hidden pages; bytes below 10 and far above 127; and all of them at
+    once in neighbouring pages."""
+    def at(table, *more):
+        return at_tokens(table, 0, token, *(token + page * m for m in more), page=page)
+
+    def nan_key(c, table):
+        c.ks[at(table)[0], 0] = 255
+
+    def nan_value(c, table):
+        c.vs[at(table)[0], 1] = 255
+
+    def hide(c, table):
+        table[0, token // page] = -1
+
+    def far(c, table):
+        p = at(table, 1, 2)
+        c.vs[p[0], 0], c.vs[p[1], 0], c.vs[p[2], 0] = 3, 190, 9
+        c.ks[p[0], 1], c.ks[p[1], 1], c.ks[p[2], 0] = 0, 9, 135
+
+    def tiny(c, table):
+        c.vs[:, 0] = 6
+
+    def mixed(c, table):
+        hide(c, table)
+        c.ks[at_tokens(table, 0, token + page, page=page)[0], 0] = 255
+        far_page = at_tokens(table, 0, token + 2 * page, page=page)[0]
+        c.vs[far_page, 1] = 200
+    for mutate in (nan_key, nan_value, hide, far, tiny, mixed):
+        run_prompt_both(gemm, 2, 2, dim, page, [n], [ctx], window, sinks, mutate=mutate)
+
+
+@pytest.mark.parametrize("scale", [3.0, 0.0, -0.3])
+def test_attend_prompt_whole_blocks_scales(gemm, scale):
+    run_prompt_both(gemm, 1, 3, 128, 64, [100], [700], scale=scale)
+    run_prompt_both(gemm, 1, 3, 64, 16, [100], [700], scale=scale)
