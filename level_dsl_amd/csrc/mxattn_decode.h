@@ -94,6 +94,7 @@ __global__ __launch_bounds__(THREADS, 2) void decode_kernel(AttnArgs p)
     if (b0 < b1) {
         here = ids_of<SMALL>(c, table, rg.start(b0), rg.hi);
         fetch_keys(here, rg.start(b0));
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);   // the waits count on this order
         fetch_values(here, rg.start(b0));
         if (b0 + WAVES < b1) next = ids_of<SMALL>(c, table, rg.start(b0 + WAVES), rg.hi);
     }
