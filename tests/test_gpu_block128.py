@@ -135,6 +135,18 @@ def test_product_native(gemm, M, N, K, fa, fb, rows_b, bf16, acc):
     assert got.isfinite().all()
 
 
+# every number of blocks behind the last whole group of four
+@pytest.mark.parametrize("variant,M,N", [(L.MXGEMM_VARIANT_LARGE, 257, 130), (L.MXGEMM_VARIANT_LARGE_NATIVE, 2561, 2310)])
+@pytest.mark.parametrize("K", [128, 256, 384, 512, 640, 880, 1024, 1920])
+@pytest.mark.parametrize("rows_b,bf16,acc", [(128, True, False), (1, False, True)])
+def test_product_large_stages(gemm, variant, M, N, K, rows_b, bf16, acc):
+    gemm.set_variant(variant)
+    try:
+        check(gemm, M, N, K, 0, 0, rows_b, bf16, acc, seed=K, native=variant == L.MXGEMM_VARIANT_LARGE_NATIVE, where=DEV)
+    finally:
+        gemm.set_variant(L.MXGEMM_VARIANT_AUTO)
+
+
 @pytest.mark.parametrize("variant", [L.MXGEMM_VARIANT_AUTO, L.MXGEMM_VARIANT_SKINNY])
 @pytest.mark.parametrize("M", [2 ** 26 - 70, 2 ** 26 + 37])
 def test_product_many_rows(gemm, variant, M):
