@@ -452,6 +452,67 @@ def test_linear_layer_step(gemm, T, I, O):
         assert abs(float(dw[o, i]) - d) <= bound + 1e-12 * abs(d)
 
 
+def quant_error(x, rows, fmt):
+    """Bound of |code * scale - x| for the quantization of x (R, K) in blocks of
+    `rows` x 128: half a step of the format (relative, or of its subnormals in
+    units of the scale) and three fp32 roundings."""
+    R, K = x.shape
+    a = torch.zeros((cdiv(R, rows) * rows, cdiv(K, 128) * 128), dtype=torch.float64)
+    a[:R, :K] = x.abs()
+    top = a.view(-1, rows, cdiv(K, 128), 128).amax(dim=(1, 3))
+    s = (top / FMAX[fmt]).repeat_interleave(rows, 0)[:R].repeat_interleave(128, 1)[:, :K]
+    half, sub = (2.0 ** -4, 2.0 ** -10) if fmt == 0 else (2.0 ** -3, 2.0 ** -17)
+    return torch.maximum(half * x.abs(), sub * s) + 3 * 2.0 ** -23 * x.abs()
+
+
+@pytest.mark.parametrize("T,I,O", [(256, 256, 256), (37, 272, 144)])
+def test_linear_layer_gradients(gemm, T, I, O):
+    """y, dx and dw against x w^T, dy w and dy^T x of the factors before their
+    quantization, in fp64, and dx and dw against differences of the loss <x w^T,
+    dy> taken through the forward.  All entries are positive and their size
+    goes up and down along every axis at a pace of its own, so that the bound
+    (every factor off by its quantization's half step, the product's own, the
+    output's rounding) is a fraction of each result, and a factor that is
+    swapped, turned or left out is far outside it."""
+    g = torch.Generator().manual_seed(T)
+    wave = lambda n, p: torch.exp2((torch.arange(n) % p).double())
+    fac = lambda r, c, p, q: (0.5 + torch.rand((r, c), generator=g).double()) * wave(r, p)[:, None] * wave(c, q)
+    x, w, dy = fac(T, I, 3, 5).bfloat16(), fac(O, I, 4, 3).float(), fac(T, O, 5, 3).bfloat16()
+    y, dx, dw, _ = linear_step(gemm, x.to(DEV), w.to(DEV), dy.to(DEV))
+    y, dx, dw = (t.double().cpu() for t in (y, dx, dw))
+    x, w, dy = x.double(), w.double(), dy.double()
+
+    def bound(a, ea, b, eb, bf16):
+        """of a b^T, a and b off by ea and eb"""
+        t = ea @ b.t() + a @ eb.t() + ea @ eb.t()
+        ref = a @ b.t()
+        t = t + (cdiv(a.shape[1], 128) + 16) * 2.0 ** -24 * (ref + t)
+        return ref, t + 2.0 ** -8 * (ref + t) if bf16 else t
+    got = {"y": y, "dx": dx, "dw": dw}
+    ew = quant_error(w, 128, 0)
+    want = {"y": bound(x, quant_error(x, 1, 0), w, ew, True),
+            "dx": bound(dy, quant_error(dy, 1, 1), w.t(), ew.t(), True),
+            "dw": bound(dy.t(), quant_error(dy.t(), 1, 1), x.t(), quant_error(x.t(), 1, 0), False)}
+    for name, (ref, tol) in want.items():
+        assert (tol < 0.25 * ref).all()
+        assert ((got[name] - ref).abs() <= tol).all(), name
+        if T == I == O:         # the bound tells every result from its transpose and from the others
+            for other in ("y", "dx", "dw"):
+                for r in (want[other][0], want[other][0].t()):
+                    assert r is ref or int(((r - ref).abs() > tol).sum()) > T * T // 2
+    loss = lambda x, w: float(((x @ w.t()) * dy).sum())
+    for o, i in ((0, 0), (O - 1, I - 1), (O // 2, 3)):
+        e = torch.zeros_like(w)
+        e[o, i] = 0.25
+        d = (loss(x, w + e) - loss(x, w - e)) / 0.5
+        assert abs(float(dw[o, i]) - d) <= float(want["dw"][1][o, i]) + 1e-6 * abs(d)
+    for t, i in ((0, 0), (T - 1, I - 1), (T // 2, 3)):
+        e = torch.zeros_like(x)
+        e[t, i] = 0.25
+        d = (loss(x + e, w) - loss(x - e, w)) / 0.5
+        assert abs(float(dx[t, i]) - d) <= float(want["dx"][1][t, i]) + 1e-6 * abs(d)
+
+
 def test_captured_step(gemm):
     """quantize and the three products in one captured graph, replayed over new
     inputs in the same buffers, with eager work between the replays."""
