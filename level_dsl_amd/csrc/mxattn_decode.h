@@ -21,8 +21,12 @@
 // The waves share nothing until the end: each streams its blocks through LDS
 // buffers of its own (keys, values) by direct-to-LDS loads: whole lines, no
 // registers, no barrier.  A block's keys are loaded while the block before is
-// in its softmax and second product, its values behind that product; with two
-// waves per SIMD one computes while the other waits.  (Two buffers of both,
+// in its softmax and second product, its values behind that product.  As
+// compiled, the loop ends with a wait for all of them (the values' scale byte
+// changes registers there, which waits for every load before it), so the values,
+// and what is left of the keys, are hidden by the other of the SIMD's two waves
+// only.  The waits that the kernel itself asks for count on the order: keys
+// first, values behind them.  (Two buffers of both,
 // one wave per SIMD: 210 us where this takes 153 us, 64 sequences of 4097 to
 // 8192 tokens, 64 / 8 heads, dim 128: 5.35 TB/s.)  The running maximum lags: it moves, and
 // what was summed is scaled, only where a score passes it by more than 8

@@ -5,7 +5,13 @@
 // group) pairs, in token order), 32 a wave, and walks the visible keys in
 // blocks of 64, whose keys and values the waves load into one of two LDS
 // buffers together while the other is used: as codes, so that a read moves
-// half the bytes; each wave widens what it reads.  Per block a wave computes
+// half the bytes; each wave widens what it reads.  As compiled, a wave's own
+// work hides little of these loads: with pages of 64 and more a block's scale
+// bytes are wave-uniform, so the compiler moves them to scalar registers as
+// soon as they are asked for, and waits for the whole block with them (loads
+// return in order) before it starts on the one at hand; with smaller pages the
+// bytes stay per lane and that wait stands behind the first product.  The
+// SIMD's other wave computes meanwhile.  Per block a wave computes
 //   S^T = K Q^T, O^T += V^T P^T     32x32x16 bf16 MFMA
 // with a row in each MFMA column (lane l: row l % 32, lane half h = l / 32).
 // As in the decode kernel the softmax needs no exchange of data: the token

@@ -27,12 +27,14 @@
 // [stage][row] order in LDS, so that a lane's rows are one conflict-free
 // read.  With 128 x 128 blocks, B's scale is one scalar per wave and stage.
 //
-// Measured (e4m3): native, 8192^3, bf16 out 455-485 us (2.3-2.4 PFLOP/s): one FMA
-// per output and stage beside the MFMAs (128 against 32 of 16 cycles, per
-// wave), at the clock that this load is held to.  Exact, 4096^3, bf16 out 119 us
-// (1.15 PFLOP/s); with a scale per row of B and fp32 out 135 us: the widening
-// (128 conversions) and the scales' 64 or 128 instructions beside 64 MFMAs of 16
-// cycles.
+// Measured (e4m3, calls behind each other until the clock has settled; traced in
+// short runs right after other work they take 7 to 14 % more): native, 8192^3,
+// bf16 out 457 us (2.4 PFLOP/s): one FMA per output and stage beside the MFMAs
+// (128 against 32 of 16 cycles, per wave), at the clock that this load is held
+// to.  Exact, 4096^3, bf16 out 121 us (1.14 PFLOP/s); with a scale per row of B
+// and fp32 out 136 us: the widening (128 conversions) and the scales' 64 or 128
+// instructions beside 64 MFMAs of 16 cycles.  All three wait for A at every
+// stage (main loop).
 #pragma once
 
 #include "mxblock.h"
@@ -70,7 +72,9 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(block::Args p)
     constexpr int BN = columns<NATIVE>(), NT = BN / 32;   // column tiles of a wave
     constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK;
     constexpr int A_SEGS = A_BYTES / 1024 / WAVES, B_SEGS = B_BYTES / 1024 / WAVES;
-    // separate objects, so that a read of one does not wait for loads into another
+    // separate objects: a read of which the compiler knows the object does not
+    // wait for loads into another (scale_a's reads lose that record, see the
+    // main loop)
     __shared__ __attribute__((aligned(1024))) uint8_t a0[A_BYTES], a1[A_BYTES], b0[B_BYTES], b1[B_BYTES];
     __shared__ float scale_a[2][4][BM];
     __shared__ float scale_b[ROWS_B == 1 ? 2 : 1][ROWS_B == 1 ? 4 : 1][ROWS_B == 1 ? BN : 1];
@@ -245,7 +249,12 @@ __global__ __launch_bounds__(THREADS, 2) void kernel(block::Args p)
     // Stage kt's first half loads B of stage kt + 1, a load a step (a burst of
     // them backs up the address path and stalls the waves behind it).  By its
     // middle every wave holds its A rows in registers, so after a barrier
-    // there the second half loads A of stage kt + 2 over stage kt's.
+    // there the second half loads A of stage kt + 2 over stage kt's.  The counted
+    // wait at a stage's end lets those stay in flight; as compiled, the next
+    // stage begins with a wait for all of them all the same, because its reads
+    // of scale_a are taken to be of any LDS object, and because at the loop's
+    // head the loads of every conditional stage count as in flight.  A thus has
+    // half a stage to arrive in, not one and a half.
     auto sb_of = [&](int kt) MXG_INLINE -> float {
         if constexpr (ROWS_B == 1) return 0.0f;
         return scalar_load(bs + min(kt, KB - 1));

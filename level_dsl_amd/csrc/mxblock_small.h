@@ -26,7 +26,7 @@
 // block are one dword load (lane l: row l), handed out by lane exchanges.
 //
 // Bound by the bytes that move from the L2s into LDS, about 50 GB/s a CU: a
-// 64 x 64 tile reads 16 KB for 2^20 products.  The workgroups of one XCD take
+// 64 x 64 tile reads 16 KB for 2^19 products.  The workgroups of one XCD take
 // neighbouring tiles, so that its L2 reads few columns of B (333 x 3584 x 4112:
 // 24 us, 30 with tiles dealt in order).
 #pragma once

@@ -133,6 +133,9 @@ Plan plan_of(const mxgemm_cache *c, const mxgemm_batch *b, int q_heads, int64_t 
     //   8 x 128 rows, 128 keys, 8 heads  8.8 / 9.7 [512 x 1]       64 x 80 rows, 40 keys, 8 heads  29 / 12 [2560 x 1]
     //   49 x 72 rows, 72 keys, 4 heads  14 / 9.2 [980 x 1]         5 x 916 rows, 229 keys, 8 heads  24 / 16 [2320 x 2]
     //   16 x 32 rows, 8192 keys, 8 heads  77 / 98, 48 rows: 109 / 114
+    // The limit of 24000 lies between [128 x 128] and [192 x 128]; two pairs of
+    // fewer blocks, [512 x 60] and [1024 x 28], take the prompt kernel by it
+    // although the other is 8 to 9 % faster there.
     const int64_t small = tiles_of(c, b, q_heads, mxg::kDecodeRows);
     const int64_t seen = windowed ? blocks_of(mxg::kDecodeRows) : (reach - std::min(tokens, reach) / 2 + 63) / 64;
     p.prompt = rows_of(c, b, q_heads) > 48 && (heads * small > 24000 / seen || (heads * small > 900 && seen <= 8));
