@@ -619,3 +619,24 @@ def test_attend_prompt_interior_special(gemm, dim, page, window, sinks, n, ctx, 
 def test_attend_prompt_whole_blocks_scales(gemm, scale):
     run_prompt_both(gemm, 1, 3, 128, 64, [100], [700], scale=scale)
     run_prompt_both(gemm, 1, 3, 64, 16, [100], [700], scale=scale)
+
+
+@pytest.mark.parametrize("n,ctx", [([2, 1], [40, 9]), ([90, 5], [300, 5])])
+def test_rows_before_the_first_sequence(gemm, n, ctx):
+    """q_start may begin past zero: the rows before it belong to no sequence."""
+    off, heads, dim, page = 3, 2, 64, 16
+    table, q, cl, pages = ref.batch(len(n), n, ctx, page, 3)
+    c = ref.Cache(pages, heads, page, dim, 4)
+    fill(c, table, q, cl - torch.tensor(n), 8)
+    T = off + sum(n)
+    K, V, Q = (rand((T, h, dim), s).bfloat16() for h, s in ((heads, 1), (heads, 2), (4 * heads, 3)))
+    kv = upload(gemm, c)
+    c.append(table, q + off, cl, K, V)
+    b = L.Batch(table.to(DEV), (q + off).to(DEV), cl.to(DEV), max_q=max(n))
+    kv.append(b, K.to(DEV), V.to(DEV))
+    same(kv, c)
+    out = torch.full((T, 4 * heads, dim), 3.0, dtype=torch.bfloat16, device=DEV)
+    ls = torch.full((T, 4 * heads), 3.0, device=DEV)
+    kv.attend(b, Q.to(DEV), out=out, lse=ls)
+    assert (out[:off] == 3.0).all() and (ls[:off] == 3.0).all()
+    compare(out[off:], ls[off:], *(x[off:] for x in ref.attend(c, table, q + off, cl, Q, dim ** -0.5, 0, 0)), sum(n))
